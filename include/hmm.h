@@ -380,6 +380,49 @@ hmm_status hmm_quant_rows_group(const void* x, int64_t T, int64_t H, uint8_t* xq
 hmm_status hmm_quant_cols_group(const void* w, int64_t E, int64_t H, int64_t N, uint8_t* wq, float* dsw,
                                 void* stream);
 
+/* The norms before and after a block, fused with the block's gate and the residual
+ * sum.  With y the output of a block (hmm_forward, hmm_moe_decode, any projection),
+ * r the residual stream before it, wp and w the two norms' weights, g the block's
+ * gate and s = residual_scale:
+ *   u  = y / sqrt(mean_H(y^2) + eps)       (u = y where post_weight is NULL)
+ *   r' = r + s * g * wp * u                rounded to residual_dtype and stored
+ *   n  = r' / sqrt(mean_H(r'^2) + eps) * w   of the stored r', bf16
+ * n is the input of the next block.  With y = NULL the call is the first norm of a
+ * stack: n alone, of ``residual`` (post_weight, residual_out NULL, no gate).
+ *   y            bf16 [T,H]
+ *   residual     residual_dtype [T,H]
+ *   norm_weight, post_weight   weight_dtype [H]
+ *   gate         bf16; HMM_GATE_TOKEN [T], HMM_GATE_CHANNEL [H], HMM_GATE_FULL [T,H]
+ *   residual_out residual_dtype [T,H], may be ``residual`` itself
+ *   normed       bf16 [T,H], may be ``y`` itself
+ *   rstd         float32 [2,T] (1/sqrt of the post-norm and of the pre-norm) for the
+ *                backward, or NULL
+ * T >= 0 rows; H a multiple of 8 in [8, 16384].  All arithmetic is float32.
+ *
+ * The backward takes the gradients of the two outputs (either may be NULL: zero) and
+ * the stored residual_out, and writes d_y, d_residual (residual_dtype), d_norm_weight
+ * and d_post_weight (weight_dtype), d_gate (bf16, the gate's shape); those of absent
+ * inputs are NULL.  Column sums are added in a fixed order.  With y = NULL,
+ * ``residual_out`` is the forward's ``residual``. */
+typedef enum hmm_gate_kind { HMM_GATE_NONE = 0, HMM_GATE_TOKEN = 1, HMM_GATE_CHANNEL = 2, HMM_GATE_FULL = 3 } hmm_gate_kind;
+typedef struct hmm_norm_problem {
+  int64_t T, H;
+  int32_t residual_dtype;  /* HMM_BF16 or HMM_F32 */
+  int32_t weight_dtype;    /* HMM_BF16 or HMM_F32 */
+  int32_t gate_kind;
+  float eps;               /* a positive normal float32 */
+  float residual_scale;
+} hmm_norm_problem;
+hmm_status hmm_residual_norm(const hmm_norm_problem* p, const void* y, const void* residual, const void* norm_weight,
+                             const void* post_weight, const void* gate, void* residual_out, void* normed, float* rstd,
+                             void* stream);
+hmm_status hmm_residual_norm_backward_sizes(const hmm_norm_problem* p, size_t* workspace_bytes);
+hmm_status hmm_residual_norm_backward(const hmm_norm_problem* p, const void* d_residual_out, const void* d_normed,
+                                      const void* y, const void* residual_out, const void* norm_weight,
+                                      const void* post_weight, const void* gate, const float* rstd, void* d_y,
+                                      void* d_residual, void* d_norm_weight, void* d_post_weight, void* d_gate,
+                                      void* workspace, size_t workspace_bytes, void* stream);
+
 /* Names of statuses, and the calling thread's last error text. */
 const char* hmm_status_string(hmm_status s);
 const char* hmm_last_error_message(void);

@@ -29,6 +29,7 @@ HMM_FLAG_TILES_NARROW = 4
 HMM_FLAG_FUSED_FORWARD = 8
 HMM_FLAG_SERIAL_BACKWARD = 16
 HMM_FLAG_FP8_BACKWARD = 32
+HMM_GATE_NONE, HMM_GATE_TOKEN, HMM_GATE_CHANNEL, HMM_GATE_FULL = 0, 1, 2, 3
 TILE_FLAGS = {"auto": 0, "large": HMM_FLAG_TILES_LARGE, "narrow": HMM_FLAG_TILES_NARROW}
 
 # every symbol include/hmm.h declares
@@ -38,6 +39,7 @@ EXPORTS = (
     "hmm_profile_enable", "hmm_profile_read", "hmm_quant_rows_fp8", "hmm_quant_cols_workspace_size",
     "hmm_quant_cols_fp8", "hmm_forward_shared", "hmm_backward_shared", "hmm_quant_rows_mx", "hmm_quant_cols_mx",
     "hmm_quant_rows_group", "hmm_quant_cols_group", "hmm_set_fused_spin_limit", "hmm_forward_noalloc",
+    "hmm_residual_norm", "hmm_residual_norm_backward_sizes", "hmm_residual_norm_backward",
 )
 
 
@@ -57,12 +59,19 @@ class StageTime(ctypes.Structure):
     _fields_ = [("name", ctypes.c_char * 32), ("launches", ctypes.c_int32), ("ms", ctypes.c_double)]
 
 
+class NormProblem(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("H", ctypes.c_int64), ("residual_dtype", ctypes.c_int32),
+                ("weight_dtype", ctypes.c_int32), ("gate_kind", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("residual_scale", ctypes.c_float)]
+
+
 _lock = threading.Lock()
 _lib = None
 
 _P = ctypes.c_void_p
 _SZ = ctypes.c_size_t
 _PROB = ctypes.POINTER(Problem)
+_NORM = ctypes.POINTER(NormProblem)
 _SIGS = {
     "hmm_forward_sizes": [_PROB, ctypes.POINTER(_SZ), ctypes.POINTER(_SZ)],
     "hmm_saved_layout_of": [_PROB, ctypes.POINTER(SavedLayout)],
@@ -81,6 +90,9 @@ _SIGS = {
     "hmm_quant_cols_mx": [_P, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, _P, _P, _P],
     "hmm_quant_rows_group": [_P, ctypes.c_int64, ctypes.c_int64, _P, _P, _P],
     "hmm_quant_cols_group": [_P, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, _P, _P, _P],
+    "hmm_residual_norm": [_NORM] + [_P] * 9,
+    "hmm_residual_norm_backward_sizes": [_NORM, ctypes.POINTER(_SZ)],
+    "hmm_residual_norm_backward": [_NORM] + [_P] * 14 + [_SZ, _P],
     "hmm_status_string": [ctypes.c_int],
     "hmm_set_fused_spin_limit": [ctypes.c_uint32],
     "hmm_last_error_message": [],

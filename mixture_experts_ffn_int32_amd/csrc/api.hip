@@ -1224,6 +1224,106 @@ hmm_status hmm_quant_cols_group(const void* w, int64_t E, int64_t H, int64_t N, 
 
 }  // extern "C"
 
+// ------------------------------------------------------------- norms around a block
+namespace {
+size_t norm_workspace(const hmm_norm_problem* p) { return up((size_t)hmm::norm_partial_rows(p->T, p->H) * p->H * 4 * 3); }
+
+hmm_status validate_norm(const hmm_norm_problem* p, bool block, hmm::NormArgs* a) {
+  if (!p) return fail(HMM_ERR_NULL_POINTER, "problem is NULL");
+  if (p->T < 0 || p->T > (int64_t)0x7fffffff) return fail(HMM_ERR_BAD_SHAPE, "T must be in [0, 2^31) (got %lld)", (long long)p->T);
+  if (p->H < 8 || p->H % 8 || p->H > hmm::NORM_MAX_H)
+    return fail(HMM_ERR_BAD_SHAPE, "H must be a multiple of 8 in [8, %lld] (got %lld)", (long long)hmm::NORM_MAX_H, (long long)p->H);
+  for (int32_t t : {p->residual_dtype, p->weight_dtype})
+    if (t != HMM_BF16 && t != HMM_F32) return fail(HMM_ERR_BAD_DTYPE, "residual_dtype and weight_dtype must be HMM_BF16 or HMM_F32");
+  if (p->gate_kind < HMM_GATE_NONE || p->gate_kind > HMM_GATE_FULL || (p->gate_kind != HMM_GATE_NONE && !block))
+    return fail(HMM_ERR_BAD_SHAPE, "unknown gate_kind %d, or a gate without y", p->gate_kind);
+  if (!(p->eps >= 1.17549435e-38f) || !(p->eps <= 3.40282347e38f)) return fail(HMM_ERR_BAD_SHAPE, "eps must be a positive normal float32");
+  if (!(p->residual_scale >= -3.40282347e38f) || !(p->residual_scale <= 3.40282347e38f)) return fail(HMM_ERR_BAD_SHAPE, "residual_scale must be finite");
+  *a = hmm::NormArgs{};
+  a->T = p->T;
+  a->H = p->H;
+  a->res_f32 = p->residual_dtype == HMM_F32;
+  a->w_f32 = p->weight_dtype == HMM_F32;
+  a->gate_kind = p->gate_kind;
+  a->eps = p->eps;
+  a->scale = p->residual_scale;
+  return HMM_OK;
+}
+}  // namespace
+
+extern "C" {
+
+hmm_status hmm_residual_norm(const hmm_norm_problem* p, const void* y, const void* residual, const void* norm_weight,
+                             const void* post_weight, const void* gate, void* residual_out, void* normed, float* rstd,
+                             void* stream) {
+  hmm::NormArgs a;
+  hmm_status s = validate_norm(p, y != nullptr || p == nullptr || p->T == 0, &a);
+  if (s != HMM_OK) return s;
+  const bool ne = p->T > 0;
+  if (!y && (post_weight || residual_out)) {
+    if (ne) return fail(HMM_ERR_BAD_SHAPE, "post_weight and residual_out need y");
+  }
+  if ((s = need(y, false, "y")) || (s = need(residual, ne, "residual")) || (s = need(norm_weight, true, "norm_weight")) ||
+      (s = need(post_weight, false, "post_weight")) || (s = need(gate, ne && p->gate_kind != HMM_GATE_NONE, "gate")) ||
+      (s = need(residual_out, ne && y, "residual_out")) || (s = need(normed, ne, "normed")) || (s = need(rstd, false, "rstd")))
+    return s;
+  a.y = (const uint16_t*)y;
+  a.residual = residual;
+  a.norm_weight = norm_weight;
+  a.post_weight = post_weight;
+  a.gate = (const uint16_t*)gate;
+  a.residual_out = residual_out;
+  a.normed = (uint16_t*)normed;
+  a.rstd = rstd;
+  Stage stage("residual_norm", (hipStream_t)stream);
+  const hipError_t e = hmm::launch_residual_norm(a, (hipStream_t)stream);
+  return e == hipSuccess ? HMM_OK : hip_fail(e, "residual norm launch");
+}
+
+hmm_status hmm_residual_norm_backward_sizes(const hmm_norm_problem* p, size_t* workspace_bytes) {
+  hmm::NormArgs a;
+  const hmm_status s = validate_norm(p, true, &a);
+  if (s != HMM_OK) return s;
+  if (!workspace_bytes) return fail(HMM_ERR_NULL_POINTER, "workspace_bytes is NULL");
+  *workspace_bytes = norm_workspace(p);
+  return HMM_OK;
+}
+
+hmm_status hmm_residual_norm_backward(const hmm_norm_problem* p, const void* d_residual_out, const void* d_normed,
+                                      const void* y, const void* residual_out, const void* norm_weight,
+                                      const void* post_weight, const void* gate, const float* rstd, void* d_y,
+                                      void* d_residual, void* d_norm_weight, void* d_post_weight, void* d_gate,
+                                      void* workspace, size_t workspace_bytes, void* stream) {
+  hmm::NormArgs a;
+  hmm_status s = validate_norm(p, y != nullptr || p == nullptr || p->T == 0, &a);
+  if (s != HMM_OK) return s;
+  const bool ne = p->T > 0;
+  if (ne && !y && post_weight) return fail(HMM_ERR_BAD_SHAPE, "post_weight needs y");
+  const bool gated = p->gate_kind != HMM_GATE_NONE;
+  if ((s = need(d_residual_out, false, "d_residual_out")) || (s = need(d_normed, false, "d_normed")) || (s = need(y, false, "y")) ||
+      (s = need(residual_out, ne, "residual_out")) || (s = need(norm_weight, true, "norm_weight")) ||
+      (s = need(post_weight, false, "post_weight")) || (s = need(gate, ne && gated, "gate")) || (s = need(rstd, ne, "rstd")) ||
+      (s = need(d_y, ne && y, "d_y")) || (s = need(d_residual, ne, "d_residual")) ||
+      (s = need(d_norm_weight, true, "d_norm_weight")) || (s = need(d_post_weight, post_weight != nullptr, "d_post_weight")) ||
+      (s = need(d_gate, gated && (ne || p->gate_kind == HMM_GATE_CHANNEL), "d_gate")) || (s = need(workspace, ne, "workspace")))
+    return s;
+  if (workspace_bytes < norm_workspace(p))
+    return fail(HMM_ERR_WORKSPACE_TOO_SMALL, "workspace is %zu bytes, %zu needed", workspace_bytes, norm_workspace(p));
+  a.y = (const uint16_t*)y;
+  a.residual = residual_out;
+  a.norm_weight = norm_weight;
+  a.post_weight = post_weight;
+  a.gate = (const uint16_t*)gate;
+  a.rstd = const_cast<float*>(rstd);
+  const hmm::NormGradArgs g{d_residual_out, (const uint16_t*)d_normed, (uint16_t*)d_y, d_residual, d_norm_weight,
+                            d_post_weight, d_gate, (float*)workspace};
+  Stage stage("residual_norm_bwd", (hipStream_t)stream);
+  const hipError_t e = hmm::launch_residual_norm_bwd(a, g, (hipStream_t)stream);
+  return e == hipSuccess ? HMM_OK : hip_fail(e, "residual norm backward launch");
+}
+
+}  // extern "C"
+
 // ------------------------------------------------------------- no-allocation forward
 // hmm_forward_noalloc takes its workspace from this file-scope device array:
 // one copy per device, held from the library's load on that device until the

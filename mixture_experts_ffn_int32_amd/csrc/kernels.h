@@ -285,4 +285,37 @@ hipError_t launch_combine_dx_f32(const float* rows, const int32_t* row_of_slot, 
 // x float32 [n][H] -> bf16 [n][2H] = [hi | lo]
 hipError_t launch_split_rows(const float* x, int64_t n, int64_t H, uint16_t* out, hipStream_t stream);
 
+// Norms around a block (norm.hip): r' = round(r + s g wp rms(y)), n = rms(r') w, and the gradients.
+constexpr int64_t NORM_MAX_H = 16384;  // a row stays in one workgroup's registers
+enum NormGate { NORM_GATE_NONE = 0, NORM_GATE_TOKEN = 1, NORM_GATE_CHANNEL = 2, NORM_GATE_FULL = 3 };
+struct NormArgs {
+  int64_t T, H;
+  bool res_f32, w_f32;       // types of the residual stream and of the two weights (else bf16)
+  int gate_kind;
+  float eps, scale;
+  const uint16_t* y;         // [T][H], or NULL: n = rms(residual) w alone
+  const void* residual;      // r; in the backward the stored r'
+  const void* norm_weight;   // [H]
+  const void* post_weight;   // [H] or NULL
+  const uint16_t* gate;      // [T], [H] or [T][H] by gate_kind
+  void* residual_out;
+  uint16_t* normed;
+  float* rstd;               // [2][T]: rho_y, rho (NULL in a forward: not stored)
+};
+struct NormGradArgs {
+  const void* d_residual_out;   // NULL: zero
+  const uint16_t* d_normed;     // NULL: zero
+  uint16_t* d_y;
+  void* d_residual;
+  void *d_norm_weight, *d_post_weight, *d_gate;
+  float* partial;               // [3][norm_partial_rows][H]
+};
+struct NormSums {
+  void* out[3];
+  bool f32[3];
+};
+int64_t norm_partial_rows(int64_t T, int64_t H);
+hipError_t launch_residual_norm(const NormArgs& A, hipStream_t stream);
+hipError_t launch_residual_norm_bwd(const NormArgs& A, const NormGradArgs& G, hipStream_t stream);
+
 }  // namespace hmm

@@ -1,0 +1,383 @@
+// The norms before and after a block, fused with the block's gate and the
+// residual sum, and their gradients.
+//
+//   u  = y rho_y,  rho_y = (mean_H y^2 + eps)^-1/2      (post-norm; u = y without a post weight)
+//   r' = round(r + s g wp u)                            (the residual stream as it is stored)
+//   n  = r' rho w, rho   = (mean_H r'^2 + eps)^-1/2     (the next block's pre-norm)
+//
+// and, with t the whole gradient of r' (tr that of its output, dn that of n):
+//   a  = dn w;   t = tr + rho a - r' rho^3 mean(a r');  dr = t
+//   b  = s t g wp;  dy = rho_y b - y rho_y^3 mean(b y)  (dy = b without a post weight)
+//   dw = sum_t dn r' rho;  dwp = sum_t s t g u;  dg = s t wp u, summed over what g is broadcast over
+//
+// n is taken of the stored (rounded) r', so that the backward, which reads the
+// stored r', is the gradient of exactly what the forward computed.
+//
+// All of it is bound by HBM: a row is read once, kept in registers between the
+// reductions (two in the forward, two in the backward), and written once; every
+// sum is float32.  A row belongs to one wave (H <= 1024) or one workgroup, V
+// 16-byte chunks per thread.  The backward's column sums stay in registers
+// while a workgroup walks its rows (one fixed set of workgroups, whatever the
+// device), then go to the workspace as one partial row per workgroup, and a
+// second launch adds those in order: no atomics, the same bits on every run.
+#include "device.h"
+#include "kernels.h"
+
+namespace hmm {
+namespace {
+
+constexpr int MAX_THREADS_PER_ROW = 1024;
+
+// 8 consecutive elements at index i of a bf16 or float32 array
+__device__ __forceinline__ void load8(const void* p, bool f32, int64_t i, float (&v)[8]) {
+  if (f32) {
+    const f32x4* q = reinterpret_cast<const f32x4*>(static_cast<const float*>(p) + i);
+    const f32x4 a = q[0], b = q[1];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[j] = a[j];
+      v[4 + j] = b[j];
+    }
+  } else {
+    unpack8(*reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(p) + i), v);
+  }
+}
+__device__ __forceinline__ void store8(void* p, bool f32, int64_t i, const float (&v)[8]) {
+  if (f32) {
+    f32x4* q = reinterpret_cast<f32x4*>(static_cast<float*>(p) + i);
+    q[0] = f32x4{v[0], v[1], v[2], v[3]};
+    q[1] = f32x4{v[4], v[5], v[6], v[7]};
+  } else {
+    *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p) + i) = pack8(v);
+  }
+}
+
+// 1 / sqrt(m): the hardware's v_rsq_f32 (one ulp) and one Newton step
+__device__ __forceinline__ float rsqrt_(float m) {
+  const float r = __builtin_amdgcn_rsqf(m);
+  const float c = __builtin_fmaf(0.5f * r, __builtin_fmaf(-m * r, r, 1.0f), r);
+  return __builtin_isfinite(c) ? c : r;  // m = 0 (eps = 0) or infinite: the step would make a NaN of it
+}
+
+// sums of N values over the NT threads of a row, in a fixed order, to every thread
+template <int NT, int N>
+__device__ __forceinline__ void row_sum(float (&v)[N], float* lds) {
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1)
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] += __shfl_xor(v[k], d);
+  if constexpr (NT > 64) {
+    constexpr int NW = NT / 64;
+    __syncthreads();  // the previous reduction's values have been read
+    if ((threadIdx.x & 63) == 0)
+#pragma unroll
+      for (int k = 0; k < N; ++k) lds[(threadIdx.x >> 6) * N + k] = v[k];
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      float s = 0.f;
+#pragma unroll
+      for (int q = 0; q < NW; ++q) s += lds[q * N + k];
+      v[k] = s;
+    }
+  }
+}
+
+// gate of 8 columns of row t
+__device__ __forceinline__ void gate8(const NormArgs& A, int64_t t, int64_t i, float (&g)[8]) {
+  if (A.gate_kind == NORM_GATE_TOKEN) {
+    const float v = bf2f(A.gate[t]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) g[j] = v;
+  } else if (A.gate_kind == NORM_GATE_CHANNEL) {
+    load8(A.gate, false, i, g);
+  } else if (A.gate_kind == NORM_GATE_FULL) {
+    load8(A.gate, false, t * A.H + i, g);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) g[j] = 1.f;
+  }
+}
+
+template <int NT>
+constexpr int rows_per_block() { return NT == 64 ? 4 : 1; }
+
+template <int NT, int V>
+__global__ void __launch_bounds__(NT == 64 ? 256 : NT) residual_norm_fwd(const NormArgs A) {
+  constexpr int RPB = rows_per_block<NT>();
+  __shared__ float lds[MAX_THREADS_PER_ROW / 64];
+  const int tid = NT == 64 ? (threadIdx.x & 63) : threadIdx.x;
+  const int slot = NT == 64 ? threadIdx.x >> 6 : 0;
+  const float invH = 1.f / (float)A.H;
+  for (int64_t t = (int64_t)blockIdx.x * RPB + slot; t < A.T; t += (int64_t)gridDim.x * RPB) {
+    float r[V][8], y[V][8];
+    float sum[1] = {0.f};
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      const int64_t i = (int64_t)(tid + k * NT) * 8;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) r[k][j] = y[k][j] = 0.f;
+      if (i >= A.H) continue;
+      load8(A.residual, A.res_f32, t * A.H + i, r[k]);
+      if (A.y) load8(A.y, false, t * A.H + i, y[k]);
+    }
+    if (A.y) {
+      float rho_y = 1.f;
+      if (A.post_weight) {
+#pragma unroll
+        for (int k = 0; k < V; ++k)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) sum[0] = __builtin_fmaf(y[k][j], y[k][j], sum[0]);
+        row_sum<NT>(sum, lds);
+        rho_y = rsqrt_(__builtin_fmaf(sum[0], invH, A.eps));
+      }
+      if (tid == 0 && A.rstd) A.rstd[t] = rho_y;
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        const int64_t i = (int64_t)(tid + k * NT) * 8;
+        if (i >= A.H) continue;
+        float g[8], wp[8];
+        gate8(A, t, i, g);
+        if (A.post_weight) {
+          load8(A.post_weight, A.w_f32, i, wp);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) g[j] *= rho_y * wp[j];
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          r[k][j] = __builtin_fmaf(A.scale * g[j], y[k][j], r[k][j]);
+          if (!A.res_f32) r[k][j] = round_bf(r[k][j]);
+        }
+        store8(A.residual_out, A.res_f32, t * A.H + i, r[k]);
+      }
+    }
+    sum[0] = 0.f;
+#pragma unroll
+    for (int k = 0; k < V; ++k)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum[0] = __builtin_fmaf(r[k][j], r[k][j], sum[0]);
+    row_sum<NT>(sum, lds);
+    const float rho = rsqrt_(__builtin_fmaf(sum[0], invH, A.eps));
+    if (tid == 0 && A.rstd) A.rstd[A.T + t] = rho;
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      const int64_t i = (int64_t)(tid + k * NT) * 8;
+      if (i >= A.H) continue;
+      float w[8], n[8];
+      load8(A.norm_weight, A.w_f32, i, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) n[j] = r[k][j] * rho * w[j];
+      store8(A.normed, false, t * A.H + i, n);
+    }
+  }
+}
+
+template <int NT, int V>
+__global__ void __launch_bounds__(NT == 64 ? 256 : NT) residual_norm_bwd(const NormArgs A, const NormGradArgs G) {
+  constexpr int RPB = rows_per_block<NT>();
+  __shared__ float lds[2 * MAX_THREADS_PER_ROW / 64];
+  const int tid = NT == 64 ? (threadIdx.x & 63) : threadIdx.x;
+  const int slot = NT == 64 ? threadIdx.x >> 6 : 0;
+  const float invH = 1.f / (float)A.H;
+  const bool chan = A.gate_kind == NORM_GATE_CHANNEL;
+  float cw[V][8], cp[V][8], cg[V][8];  // column sums of dw, dwp, dg
+#pragma unroll
+  for (int k = 0; k < V; ++k)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) cw[k][j] = cp[k][j] = cg[k][j] = 0.f;
+
+  for (int64_t t = (int64_t)blockIdx.x * RPB + slot; t < A.T; t += (int64_t)gridDim.x * RPB) {
+    const float rho = A.rstd[A.T + t];
+    float r[V][8], d[V][8], y[V][8], tr[V][8];
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      const int64_t i = (int64_t)(tid + k * NT) * 8;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) r[k][j] = d[k][j] = y[k][j] = tr[k][j] = 0.f;
+      if (i >= A.H) continue;
+      load8(A.residual, A.res_f32, t * A.H + i, r[k]);
+      if (G.d_normed) load8(G.d_normed, false, t * A.H + i, d[k]);
+      if (G.d_residual_out) load8(G.d_residual_out, A.res_f32, t * A.H + i, tr[k]);
+      if (A.y) load8(A.y, false, t * A.H + i, y[k]);
+    }
+    float s1[1] = {0.f};
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      const int64_t i = (int64_t)(tid + k * NT) * 8;
+      if (i >= A.H) continue;
+      float w[8];
+      load8(A.norm_weight, A.w_f32, i, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        cw[k][j] = __builtin_fmaf(d[k][j] * rho, r[k][j], cw[k][j]);
+        d[k][j] *= w[j];
+        s1[0] = __builtin_fmaf(d[k][j], r[k][j], s1[0]);
+      }
+    }
+    row_sum<NT>(s1, lds);
+    const float c1 = rho * rho * rho * s1[0] * invH;
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      const int64_t i = (int64_t)(tid + k * NT) * 8;
+      if (i >= A.H) continue;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        tr[k][j] = __builtin_fmaf(rho, d[k][j], __builtin_fmaf(-c1, r[k][j], tr[k][j]));
+      store8(G.d_residual, A.res_f32, t * A.H + i, tr[k]);
+    }
+    if (!A.y) continue;  // the same for every thread
+    const float rho_y = A.rstd[t];
+    float s2[2] = {0.f, 0.f};  // sum b y, sum s t wp u
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      const int64_t i = (int64_t)(tid + k * NT) * 8;
+      if (i >= A.H) continue;
+      float g[8], wp[8], dg[8];
+      gate8(A, t, i, g);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) wp[j] = 1.f;
+      if (A.post_weight) load8(A.post_weight, A.w_f32, i, wp);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float st = A.scale * tr[k][j], u = y[k][j] * rho_y;
+        dg[j] = st * wp[j] * u;
+        cg[k][j] += dg[j];
+        s2[1] += dg[j];
+        cp[k][j] = __builtin_fmaf(st * g[j], u, cp[k][j]);
+        tr[k][j] = st * g[j] * wp[j];  // b
+        s2[0] = __builtin_fmaf(tr[k][j], y[k][j], s2[0]);
+      }
+      if (A.gate_kind == NORM_GATE_FULL) store8(G.d_gate, false, t * A.H + i, dg);
+    }
+    row_sum<NT>(s2, lds);
+    if (A.gate_kind == NORM_GATE_TOKEN && tid == 0) static_cast<uint16_t*>(G.d_gate)[t] = f2bf(s2[1]);
+    const float c2 = A.post_weight ? rho_y * rho_y * rho_y * s2[0] * invH : 0.f;
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      const int64_t i = (int64_t)(tid + k * NT) * 8;
+      if (i >= A.H) continue;
+      float dy[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) dy[j] = __builtin_fmaf(rho_y, tr[k][j], -c2 * y[k][j]);
+      store8(G.d_y, false, t * A.H + i, dy);
+    }
+  }
+
+  // one partial row per row walker: dw, then dwp, then dg (those that are asked for)
+  const int64_t pr = (int64_t)blockIdx.x * RPB + slot, np = (int64_t)gridDim.x * RPB;
+#pragma unroll
+  for (int k = 0; k < V; ++k) {
+    const int64_t i = (int64_t)(tid + k * NT) * 8;
+    if (i >= A.H) continue;
+    float* p = G.partial + pr * A.H + i;
+    store8(p, true, 0, cw[k]);
+    p += np * A.H;
+    if (A.post_weight) {
+      store8(p, true, 0, cp[k]);
+      p += np * A.H;
+    }
+    if (chan) store8(p, true, 0, cg[k]);
+  }
+}
+
+// out[c] = sum of the np partial rows of column c, in order: 4 row groups of 64
+// columns each, then the groups.  blockIdx.y names the array.
+__global__ void __launch_bounds__(256) norm_partial_sum(const float* __restrict__ partial, int np, int64_t H,
+                                                        const NormSums S) {
+  __shared__ float part[4][64];
+  const int64_t c = (int64_t)blockIdx.x * 64 + (threadIdx.x & 63);
+  const int q = threadIdx.x >> 6;
+  const int per = (np + 3) / 4;
+  const float* p = partial + (int64_t)blockIdx.y * np * H;
+  float s = 0.f;
+  if (c < H)
+#pragma unroll 8
+    for (int r = q * per; r < min(np, (q + 1) * per); ++r) s += p[(int64_t)r * H + c];
+  part[q][threadIdx.x & 63] = s;
+  __syncthreads();
+  if (q || c >= H) return;
+  s = 0.f;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) s += part[k][threadIdx.x];
+  void* out = S.out[blockIdx.y];
+  if (S.f32[blockIdx.y])
+    static_cast<float*>(out)[c] = s;
+  else
+    static_cast<uint16_t*>(out)[c] = f2bf(s);
+}
+
+// calls f<threads per row, chunks per thread> for rows of H elements
+template <class F>
+hipError_t for_width(int64_t H, F&& f) {
+  if (H <= 512) return f.template operator()<64, 1>();
+  if (H <= 1024) return f.template operator()<64, 2>();
+  if (H <= 2048) return f.template operator()<256, 1>();
+  if (H <= 4096) return f.template operator()<512, 1>();
+  if (H <= 8192) return f.template operator()<1024, 1>();
+  return f.template operator()<1024, 2>();
+}
+
+constexpr int64_t MAX_FWD_BLOCKS = 1 << 20;
+struct FwdLaunch {
+  const NormArgs& A;
+  hipStream_t stream;
+  template <int NT, int V>
+  hipError_t operator()() {
+    constexpr int R = rows_per_block<NT>();
+    const int64_t rows = (A.T + R - 1) / R;
+    // one row per workgroup up to 2^20 workgroups (a launch holds fewer than 2^32 threads)
+    residual_norm_fwd<NT, V><<<(unsigned)(rows < MAX_FWD_BLOCKS ? rows : MAX_FWD_BLOCKS), NT == 64 ? 256 : NT, 0, stream>>>(A);
+    return hipGetLastError();
+  }
+};
+struct BwdLaunch {
+  const NormArgs& A;
+  const NormGradArgs& G;
+  int blocks;
+  hipStream_t stream;
+  template <int NT, int V>
+  hipError_t operator()() {
+    residual_norm_bwd<NT, V><<<blocks, NT == 64 ? 256 : NT, 0, stream>>>(A, G);
+    return hipGetLastError();
+  }
+};
+
+constexpr int BWD_ROW_WALKERS = 512;  // workgroups (H > 1024) or waves of the backward
+inline int bwd_blocks(int64_t T, int64_t H) {
+  const int64_t rpb = H <= 1024 ? 4 : 1;
+  const int64_t b = (T + rpb - 1) / rpb, most = H <= 1024 ? 1024 / 4 : BWD_ROW_WALKERS;
+  return (int)(b < most ? b : most);
+}
+
+}  // namespace
+
+int64_t norm_partial_rows(int64_t T, int64_t H) { return (int64_t)bwd_blocks(T, H) * (H <= 1024 ? 4 : 1); }
+
+hipError_t launch_residual_norm(const NormArgs& A, hipStream_t stream) {
+  if (A.T == 0) return hipSuccess;
+  return for_width(A.H, FwdLaunch{A, stream});
+}
+
+hipError_t launch_residual_norm_bwd(const NormArgs& A, const NormGradArgs& G, hipStream_t stream) {
+  if (A.T > 0) {
+    const hipError_t e = for_width(A.H, BwdLaunch{A, G, bwd_blocks(A.T, A.H), stream});
+    if (e != hipSuccess) return e;
+  }
+  NormSums S{};
+  int n = 0;
+  S.out[n] = G.d_norm_weight;
+  S.f32[n++] = A.w_f32;
+  if (A.post_weight) {
+    S.out[n] = G.d_post_weight;
+    S.f32[n++] = A.w_f32;
+  }
+  if (A.gate_kind == NORM_GATE_CHANNEL) {
+    S.out[n] = G.d_gate;
+    S.f32[n++] = false;
+  }
+  norm_partial_sum<<<dim3((unsigned)((A.H + 63) / 64), n), 256, 0, stream>>>(
+      G.partial, (int)norm_partial_rows(A.T, A.H), A.H, S);
+  return hipGetLastError();
+}
+
+}  // namespace hmm
