@@ -80,7 +80,8 @@ typedef enum hmm_dtype {
   HMM_F32 = 1,
   HMM_FP8_E4M3 = 2,    /* E4M3 with one float32 scale per token row / weight column */
   HMM_MXFP8_E4M3 = 3,  /* E4M3 with one E8M0 exponent per 32 elements along H (MX) */
-  HMM_FP8_E4M3_GROUP = 4  /* E4M3 with one float32 scale per 128 elements along H */
+  HMM_FP8_E4M3_GROUP = 4, /* E4M3 with one float32 scale per 128 elements along H */
+  HMM_FP8_E4M3_BLOCK = 5  /* E4M3 weights with one float32 scale per block of 128 x 128 (hmm_quant_block) */
 } hmm_dtype;
 
 /* Check topk_ids: the routing (its own launch, or on small bf16 problems the
@@ -422,6 +423,75 @@ hmm_status hmm_residual_norm_backward(const hmm_norm_problem* p, const void* d_r
                                       const void* post_weight, const void* gate, const float* rstd, void* d_y,
                                       void* d_residual, void* d_norm_weight, void* d_post_weight, void* d_gate,
                                       void* workspace, size_t workspace_bytes, void* stream);
+
+/* A whole mixture-of-experts layer for a few tokens (serving): router, up-projection,
+ * SwiGLU, down-projection and weighted sum, reading each chosen expert's weights once.
+ * No backward, nothing saved.
+ *   l[t,e] = x[t] . router_w[e], in 64 bits; topk_ids[t] = the K largest logits in
+ *   descending order (equal logits: the lower expert first; a NaN ranks last);
+ *   topk_weights = exp(l - max l) over its sum over the K chosen experts
+ *   (HMM_DECODE_RENORMALIZE) or over all E experts;
+ *   then hmm_forward's y, with a kept to 16 significant bits and one rounding of y.
+ *   x             bf16 [T,H]
+ *   router_w      router_dtype (HMM_BF16 or HMM_F32) [E,H], one row per expert; or
+ *                 NULL: topk_ids and topk_weights are inputs
+ *   topk_ids      int32 [T,K]; written with a router.  As an input, ids outside
+ *                 [0, E) are dropped, and a repeated id counts once per time.
+ *   topk_weights  float32 [T,K]; written with a router
+ *   up_w, down_w  weight_dtype HMM_BF16: [E,H,2I] and [E,I,H], as hmm_forward takes
+ *                 them; HMM_FP8_E4M3_BLOCK: codes [E,2I,H] and [E,H,I] with descales
+ *                 up_descale [E,2I/128,H/128] and down_descale [E,H/128,I/128]
+ *                 (what hmm_quant_block makes of the bf16 weights); x and a stay bf16
+ *   y             bf16 [T,H]
+ * 0 <= T <= 64 (else HMM_ERR_UNSUPPORTED); 1 <= E <= 1024; 1 <= K <= 16, and K <= E
+ * with a router; H and I multiples of 64 (HMM_FP8_E4M3_BLOCK: 128), at most 65536.
+ * The workspace may hold anything before the call and is free after it; two calls
+ * that overlap in time need one each. */
+#define HMM_DECODE_RENORMALIZE 1u
+typedef struct hmm_decode_problem {
+  int64_t T, H, I, E, K;
+  int32_t weight_dtype;
+  int32_t router_dtype;
+  uint32_t flags;
+} hmm_decode_problem;
+hmm_status hmm_moe_decode_sizes(const hmm_decode_problem* p, size_t* workspace_bytes);
+hmm_status hmm_moe_decode(const hmm_decode_problem* p, const void* x, const void* router_w, int32_t* topk_ids,
+                          float* topk_weights, const void* up_w, const float* up_descale, const void* down_w,
+                          const float* down_descale, void* y, void* workspace, size_t workspace_bytes, void* stream);
+
+/* The E4M3 product with one scale per token and group of 128 and one per 128 x 128
+ * block of the weight (a dense projection; the experts of hmm_moe_decode take the same
+ * weights).  With (xq, xs) from hmm_quant_rows_group and (codes_t, descale) from
+ * hmm_quant_block:
+ *   y[t,n] = sum_g xs[t,g] descale[n/128,g] sum_{k in g} xq[t,k] codes_t[n,k]
+ * Each group's sums are taken by the matrix instruction, scaled in float32 and added in
+ * group order; y is bf16, rounded once.
+ *
+ * hmm_quant_block: w bf16 [E,H,N], per (expert, block of 128 rows, block of 128 columns;
+ *   a last block of columns may be narrower) the rule of hmm_quant_rows_group: codes_t
+ *   [E,N,H] and / or codes [E,H,N] E4M3 bytes (NULL: not written; one at least),
+ *   descale [E,ceil(N/128),H/128] float32.
+ * hmm_matmul_fp8_block: the product of codes.
+ * hmm_linear_fp8_block: x bf16 [T,H] quantised by the rule of hmm_quant_rows_group, then
+ *   the product; for T <= 64 in one launch without workspace (forward_bytes is 0 then).
+ * hmm_linear_fp8_block_grad: of dy bf16 [T,N],
+ *   dx bf16 [T,H]: dy quantised per token and 128 of N, times the same codes (in the
+ *                  layout ``codes`` [H,N]) and descales, along N; NULL: not computed
+ *   dw bf16 [H,N]: x^T dy as a bf16 product with float32 sums; NULL: not computed
+ *   (the quantisation of x and of the weight is passed through: their derivative is
+ *   taken as 1).  T = 0 writes dw = 0.
+ * T >= 0; H a multiple of 128 in [128, 65536]; N a multiple of 16 in [16, 262144], in the
+ * gradient of 128.  dw needs x and dy below 4 GiB each (else HMM_ERR_UNSUPPORTED). */
+hmm_status hmm_quant_block(const void* w, int64_t E, int64_t H, int64_t N, uint8_t* codes_t, uint8_t* codes, float* descale,
+                           void* stream);
+hmm_status hmm_matmul_fp8_block(const uint8_t* xq, const float* xs, const uint8_t* codes_t, const float* descale, int64_t T,
+                                int64_t H, int64_t N, void* y, void* stream);
+hmm_status hmm_linear_fp8_block_sizes(int64_t T, int64_t H, int64_t N, size_t* forward_bytes, size_t* grad_bytes);
+hmm_status hmm_linear_fp8_block(const void* x, const uint8_t* codes_t, const float* descale, int64_t T, int64_t H, int64_t N,
+                                void* y, void* workspace, size_t workspace_bytes, void* stream);
+hmm_status hmm_linear_fp8_block_grad(const void* dy, const void* x, const uint8_t* codes, const float* descale, int64_t T,
+                                     int64_t H, int64_t N, void* dx, void* dw, void* workspace, size_t workspace_bytes,
+                                     void* stream);
 
 /* Names of statuses, and the calling thread's last error text. */
 const char* hmm_status_string(hmm_status s);

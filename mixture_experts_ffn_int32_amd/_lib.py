@@ -23,6 +23,7 @@ HMM_ERR_HIP = 8
 HMM_ERR_TIMEOUT = 9
 
 HMM_BF16, HMM_F32, HMM_FP8_E4M3, HMM_MXFP8_E4M3, HMM_FP8_E4M3_GROUP = 0, 1, 2, 3, 4
+HMM_FP8_E4M3_BLOCK = 5
 HMM_FLAG_VALIDATE_IDS = 1
 HMM_FLAG_TILES_LARGE = 2
 HMM_FLAG_TILES_NARROW = 4
@@ -30,6 +31,7 @@ HMM_FLAG_FUSED_FORWARD = 8
 HMM_FLAG_SERIAL_BACKWARD = 16
 HMM_FLAG_FP8_BACKWARD = 32
 HMM_GATE_NONE, HMM_GATE_TOKEN, HMM_GATE_CHANNEL, HMM_GATE_FULL = 0, 1, 2, 3
+HMM_DECODE_RENORMALIZE = 1
 TILE_FLAGS = {"auto": 0, "large": HMM_FLAG_TILES_LARGE, "narrow": HMM_FLAG_TILES_NARROW}
 
 # every symbol include/hmm.h declares
@@ -40,6 +42,8 @@ EXPORTS = (
     "hmm_quant_cols_fp8", "hmm_forward_shared", "hmm_backward_shared", "hmm_quant_rows_mx", "hmm_quant_cols_mx",
     "hmm_quant_rows_group", "hmm_quant_cols_group", "hmm_set_fused_spin_limit", "hmm_forward_noalloc",
     "hmm_residual_norm", "hmm_residual_norm_backward_sizes", "hmm_residual_norm_backward",
+    "hmm_moe_decode_sizes", "hmm_moe_decode", "hmm_quant_block", "hmm_matmul_fp8_block", "hmm_linear_fp8_block_sizes",
+    "hmm_linear_fp8_block", "hmm_linear_fp8_block_grad",
 )
 
 
@@ -65,13 +69,21 @@ class NormProblem(ctypes.Structure):
                 ("residual_scale", ctypes.c_float)]
 
 
+class DecodeProblem(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("H", ctypes.c_int64), ("I", ctypes.c_int64), ("E", ctypes.c_int64),
+                ("K", ctypes.c_int64), ("weight_dtype", ctypes.c_int32), ("router_dtype", ctypes.c_int32),
+                ("flags", ctypes.c_uint32)]
+
+
 _lock = threading.Lock()
 _lib = None
 
 _P = ctypes.c_void_p
 _SZ = ctypes.c_size_t
+_I64 = ctypes.c_int64
 _PROB = ctypes.POINTER(Problem)
 _NORM = ctypes.POINTER(NormProblem)
+_DEC = ctypes.POINTER(DecodeProblem)
 _SIGS = {
     "hmm_forward_sizes": [_PROB, ctypes.POINTER(_SZ), ctypes.POINTER(_SZ)],
     "hmm_saved_layout_of": [_PROB, ctypes.POINTER(SavedLayout)],
@@ -93,6 +105,13 @@ _SIGS = {
     "hmm_residual_norm": [_NORM] + [_P] * 9,
     "hmm_residual_norm_backward_sizes": [_NORM, ctypes.POINTER(_SZ)],
     "hmm_residual_norm_backward": [_NORM] + [_P] * 14 + [_SZ, _P],
+    "hmm_moe_decode_sizes": [_DEC, ctypes.POINTER(_SZ)],
+    "hmm_moe_decode": [_DEC] + [_P] * 10 + [_SZ, _P],
+    "hmm_quant_block": [_P, _I64, _I64, _I64, _P, _P, _P, _P],
+    "hmm_matmul_fp8_block": [_P, _P, _P, _P, _I64, _I64, _I64, _P, _P],
+    "hmm_linear_fp8_block_sizes": [_I64, _I64, _I64, ctypes.POINTER(_SZ), ctypes.POINTER(_SZ)],
+    "hmm_linear_fp8_block": [_P, _P, _P, _I64, _I64, _I64, _P, _P, _SZ, _P],
+    "hmm_linear_fp8_block_grad": [_P, _P, _P, _P, _I64, _I64, _I64, _P, _P, _P, _SZ, _P],
     "hmm_status_string": [ctypes.c_int],
     "hmm_set_fused_spin_limit": [ctypes.c_uint32],
     "hmm_last_error_message": [],

@@ -18,7 +18,7 @@ CSRC = os.path.join(PKG, "csrc")
 OUT = os.path.join(PKG, "libhmm.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 SOURCES = ["route.hip", "gemm.hip", "gemm_f32.hip", "gemm_fp8.hip", "quant.hip", "pointwise.hip", "fused.hip",
-           "norm.hip", "api.hip"]
+           "norm.hip", "decode.hip", "fp8_block.hip", "api.hip"]
 
 
 def hipcc():

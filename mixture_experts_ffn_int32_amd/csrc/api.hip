@@ -1324,6 +1324,230 @@ hmm_status hmm_residual_norm_backward(const hmm_norm_problem* p, const void* d_r
 
 }  // extern "C"
 
+// ------------------------------------------------------------- the layer for a few tokens
+namespace {
+struct DecodeWork {
+  size_t logits, a, o, count, total;
+};
+DecodeWork decode_work(const hmm_decode_problem* p, bool fp8) {
+  DecodeWork w{};
+  size_t o = 0;
+  w.logits = o; o += up((size_t)p->T * p->E * 8);
+  w.a = o;      o += up((size_t)p->T * p->K * 2 * p->I * 2);
+  w.o = o;      o += up((size_t)p->T * p->K * p->H * 4);
+  w.count = o;  o += up((size_t)hmm::decode_col_tiles(p->H, fp8) * 4);
+  w.total = o;
+  return w;
+}
+
+hmm_status validate_decode(const hmm_decode_problem* p, bool* fp8) {
+  if (!p) return fail(HMM_ERR_NULL_POINTER, "problem is NULL");
+  if (p->T < 0) return fail(HMM_ERR_BAD_SHAPE, "T must be >= 0 (got %lld)", (long long)p->T);
+  if (p->T > hmm::DECODE_MAX_TOKENS)
+    return fail(HMM_ERR_UNSUPPORTED, "T is %lld: at most %d tokens (use hmm_forward for more)", (long long)p->T, hmm::DECODE_MAX_TOKENS);
+  if (p->E < 1 || p->E > hmm::MAX_EXPERTS) return fail(HMM_ERR_BAD_SHAPE, "E must be in [1, %d] (got %lld)", hmm::MAX_EXPERTS, (long long)p->E);
+  if (p->K < 1 || p->K > 16) return fail(HMM_ERR_BAD_SHAPE, "K must be in [1, 16] (got %lld)", (long long)p->K);
+  if (p->weight_dtype != HMM_BF16 && p->weight_dtype != HMM_FP8_E4M3_BLOCK)
+    return fail(HMM_ERR_BAD_DTYPE, "weight_dtype must be HMM_BF16 or HMM_FP8_E4M3_BLOCK (got %d)", p->weight_dtype);
+  if (p->router_dtype != HMM_BF16 && p->router_dtype != HMM_F32)
+    return fail(HMM_ERR_BAD_DTYPE, "router_dtype must be HMM_BF16 or HMM_F32 (got %d)", p->router_dtype);
+  *fp8 = p->weight_dtype == HMM_FP8_E4M3_BLOCK;
+  const int64_t step = *fp8 ? 128 : 64;
+  if (p->H < step || p->H > 65536 || p->H % step || p->I < step || p->I > 65536 || p->I % step)
+    return fail(HMM_ERR_BAD_SHAPE, "H and I must be multiples of %lld in [%lld, 65536] (got %lld, %lld)", (long long)step,
+                (long long)step, (long long)p->H, (long long)p->I);
+  if (p->flags & ~(uint32_t)HMM_DECODE_RENORMALIZE) return fail(HMM_ERR_BAD_SHAPE, "unknown flags 0x%x", p->flags);
+  return HMM_OK;
+}
+}  // namespace
+
+extern "C" {
+
+hmm_status hmm_moe_decode_sizes(const hmm_decode_problem* p, size_t* workspace_bytes) {
+  bool fp8 = false;
+  const hmm_status s = validate_decode(p, &fp8);
+  if (s != HMM_OK) return s;
+  if (!workspace_bytes) return fail(HMM_ERR_NULL_POINTER, "workspace_bytes is NULL");
+  *workspace_bytes = decode_work(p, fp8).total;
+  return HMM_OK;
+}
+
+hmm_status hmm_moe_decode(const hmm_decode_problem* p, const void* x, const void* router_w, int32_t* topk_ids,
+                          float* topk_weights, const void* up_w, const float* up_descale, const void* down_w,
+                          const float* down_descale, void* y, void* workspace, size_t workspace_bytes, void* stream) {
+  bool fp8 = false;
+  hmm_status s = validate_decode(p, &fp8);
+  if (s != HMM_OK) return s;
+  if (router_w && p->K > p->E)
+    return fail(HMM_ERR_BAD_SHAPE, "K = %lld experts a token of E = %lld", (long long)p->K, (long long)p->E);
+  const bool ne = p->T > 0;
+  if ((s = need(x, ne, "x")) || (s = need(router_w, false, "router_w")) || (s = need(topk_ids, ne, "topk_ids")) ||
+      (s = need(topk_weights, ne, "topk_weights")) || (s = need(up_w, true, "up_w")) || (s = need(up_descale, fp8, "up_descale")) ||
+      (s = need(down_w, true, "down_w")) || (s = need(down_descale, fp8, "down_descale")) || (s = need(y, ne, "y")) ||
+      (s = need(workspace, ne, "workspace")))
+    return s;
+  const DecodeWork w = decode_work(p, fp8);
+  if (workspace_bytes < w.total)
+    return fail(HMM_ERR_WORKSPACE_TOO_SMALL, "workspace is %zu bytes, %zu needed", workspace_bytes, w.total);
+  if (!ne) return HMM_OK;
+  hipStream_t st = (hipStream_t)stream;
+  if (router_w) {
+    Stage stage("decode_router", st);
+    const hipError_t e = hmm::launch_router((const uint16_t*)x, router_w, p->router_dtype == HMM_F32, (int)p->T, p->H, (int)p->E,
+                                            (int)p->K, (p->flags & HMM_DECODE_RENORMALIZE) != 0,
+                                            at<double>(workspace, w.logits), topk_ids, topk_weights, st);
+    if (e != hipSuccess) return hip_fail(e, "router launch");
+  }
+  hmm::DecodeArgs a{};
+  a.T = (int)p->T;
+  a.E = (int)p->E;
+  a.K = (int)p->K;
+  a.H = p->H;
+  a.I = p->I;
+  a.wbytes = fp8 ? 1 : 2;
+  a.x = (const uint16_t*)x;
+  a.ids = topk_ids;
+  a.weights = topk_weights;
+  a.up = up_w;
+  a.down = down_w;
+  a.up_descale = up_descale;
+  a.down_descale = down_descale;
+  a.a = at<uint16_t>(workspace, w.a);
+  a.o = at<float>(workspace, w.o);
+  a.count = at<uint32_t>(workspace, w.count);
+  a.col_tiles = hmm::decode_col_tiles(p->H, fp8);
+  a.y = (uint16_t*)y;
+  Stage stage("decode_experts", st);
+  const hipError_t e = hmm::launch_moe_decode(a, fp8, st);
+  return e == hipSuccess ? HMM_OK : hip_fail(e, "decode launch");
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------- FP8 block product
+namespace {
+hmm_status block_dims(int64_t T, int64_t H, int64_t N, int64_t nstep) {
+  if (T < 0 || T > (int64_t)0x7fffffff) return fail(HMM_ERR_BAD_SHAPE, "T must be in [0, 2^31) (got %lld)", (long long)T);
+  if (H < 128 || H % 128 || H > 65536) return fail(HMM_ERR_BAD_SHAPE, "H must be a multiple of 128 in [128, 65536] (got %lld)", (long long)H);
+  if (N < nstep || N % nstep || N > 65536 * 4)
+    return fail(HMM_ERR_BAD_SHAPE, "N must be a multiple of %lld in [%lld, 262144] (got %lld)", (long long)nstep, (long long)nstep, (long long)N);
+  return HMM_OK;
+}
+struct BlockWork {
+  size_t xq, xs, total;
+};
+// codes and descales of ``rows`` rows of K elements
+BlockWork block_work(int64_t rows, int64_t K) {
+  BlockWork w{};
+  w.xs = up((size_t)rows * K);
+  w.total = w.xs + up((size_t)rows * (K / 128) * 4);
+  return w;
+}
+size_t block_grad_bytes(int64_t T, int64_t N) { return block_work(T, N).total + up(8); }
+}  // namespace
+
+extern "C" {
+
+hmm_status hmm_quant_block(const void* w, int64_t E, int64_t H, int64_t N, uint8_t* codes_t, uint8_t* codes, float* descale,
+                           void* stream) {
+  hmm_status s = block_dims(0, H, N, 16);
+  if (s != HMM_OK) return s;
+  if (E < 1 || E > hmm::MAX_EXPERTS) return fail(HMM_ERR_BAD_SHAPE, "E must be in [1, %d] (got %lld)", hmm::MAX_EXPERTS, (long long)E);
+  if ((s = need(w, true, "w")) || (s = need(codes_t, codes == nullptr, "codes_t")) || (s = need(codes, false, "codes")) ||
+      (s = need(descale, true, "descale")))
+    return s;
+  Stage stage("quant_block", (hipStream_t)stream);
+  const hipError_t e = hmm::launch_quant_block((const uint16_t*)w, E, H, N, codes_t, codes, descale, (hipStream_t)stream);
+  return e == hipSuccess ? HMM_OK : hip_fail(e, "block quantisation launch");
+}
+
+hmm_status hmm_matmul_fp8_block(const uint8_t* xq, const float* xs, const uint8_t* codes_t, const float* descale, int64_t T,
+                                int64_t H, int64_t N, void* y, void* stream) {
+  hmm_status s = block_dims(T, H, N, 16);
+  if (s != HMM_OK) return s;
+  const bool ne = T > 0;
+  if ((s = need(xq, ne, "xq")) || (s = need(xs, ne, "xs")) || (s = need(codes_t, true, "codes_t")) ||
+      (s = need(descale, true, "descale")) || (s = need(y, ne, "y")))
+    return s;
+  if (!ne) return HMM_OK;
+  Stage stage("matmul_fp8_block", (hipStream_t)stream);
+  const hipError_t e = hmm::launch_block_gemm(xq, xs, codes_t, descale, T, H, N, false, (uint16_t*)y, (hipStream_t)stream);
+  return e == hipSuccess ? HMM_OK : hip_fail(e, "FP8 block product launch");
+}
+
+hmm_status hmm_linear_fp8_block_sizes(int64_t T, int64_t H, int64_t N, size_t* forward_bytes, size_t* grad_bytes) {
+  const hmm_status s = block_dims(T, H, N, 16);
+  if (s != HMM_OK) return s;
+  if (!forward_bytes || !grad_bytes) return fail(HMM_ERR_NULL_POINTER, "forward_bytes or grad_bytes is NULL");
+  *forward_bytes = T <= hmm::BLOCK_MAX_ROWS ? 0 : block_work(T, H).total;
+  *grad_bytes = block_grad_bytes(T, N);
+  return HMM_OK;
+}
+
+hmm_status hmm_linear_fp8_block(const void* x, const uint8_t* codes_t, const float* descale, int64_t T, int64_t H, int64_t N,
+                                void* y, void* workspace, size_t workspace_bytes, void* stream) {
+  hmm_status s = block_dims(T, H, N, 16);
+  if (s != HMM_OK) return s;
+  const bool ne = T > 0, few = T <= hmm::BLOCK_MAX_ROWS;
+  if ((s = need(x, ne, "x")) || (s = need(codes_t, true, "codes_t")) || (s = need(descale, true, "descale")) ||
+      (s = need(y, ne, "y")) || (s = need(workspace, !few, "workspace")))
+    return s;
+  hipStream_t st = (hipStream_t)stream;
+  if (!ne) return HMM_OK;
+  if (few) {
+    Stage stage("linear_fp8_block", st);
+    const hipError_t e = hmm::launch_block_rows((const uint16_t*)x, codes_t, descale, (int)T, H, N, (uint16_t*)y, st);
+    return e == hipSuccess ? HMM_OK : hip_fail(e, "FP8 block product launch");
+  }
+  const BlockWork w = block_work(T, H);
+  if (workspace_bytes < w.total)
+    return fail(HMM_ERR_WORKSPACE_TOO_SMALL, "workspace is %zu bytes, %zu needed", workspace_bytes, w.total);
+  uint8_t* xq = at<uint8_t>(workspace, w.xq);
+  float* xs = at<float>(workspace, w.xs);
+  if ((s = hmm_quant_rows_group(x, T, H, xq, xs, stream)) != HMM_OK) return s;
+  return hmm_matmul_fp8_block(xq, xs, codes_t, descale, T, H, N, y, stream);
+}
+
+hmm_status hmm_linear_fp8_block_grad(const void* dy, const void* x, const uint8_t* codes, const float* descale, int64_t T,
+                                     int64_t H, int64_t N, void* dx, void* dw, void* workspace, size_t workspace_bytes,
+                                     void* stream) {
+  hmm_status s = block_dims(T, H, N, 128);
+  if (s != HMM_OK) return s;
+  const bool ne = T > 0;
+  if ((s = need(dy, ne, "dy")) || (s = need(x, ne && dw, "x")) || (s = need(codes, ne && dx, "codes")) ||
+      (s = need(descale, ne && dx, "descale")) || (s = need(dx, false, "dx")) || (s = need(dw, false, "dw")) ||
+      (s = need(workspace, ne, "workspace")))
+    return s;
+  // the weight gradient's product addresses each operand through one 4 GiB buffer
+  if (dw && (T * H >= (int64_t)1 << 31 || T * N >= (int64_t)1 << 31))
+    return fail(HMM_ERR_UNSUPPORTED, "x and dy must be below 4 GiB for the weight gradient");
+  if (workspace_bytes < block_grad_bytes(T, N))
+    return fail(HMM_ERR_WORKSPACE_TOO_SMALL, "workspace is %zu bytes, %zu needed", workspace_bytes, block_grad_bytes(T, N));
+  hipStream_t st = (hipStream_t)stream;
+  const BlockWork w = block_work(T, N);
+  if (ne && dx) {
+    uint8_t* gq = at<uint8_t>(workspace, w.xq);
+    float* gs = at<float>(workspace, w.xs);
+    if ((s = hmm_quant_rows_group(dy, T, N, gq, gs, stream)) != HMM_OK) return s;
+    Stage stage("matmul_fp8_block_dx", st);
+    const hipError_t e = hmm::launch_block_gemm(gq, gs, codes, descale, T, N, H, true, (uint16_t*)dx, st);
+    if (e != hipSuccess) return hip_fail(e, "FP8 block product launch");
+  }
+  if (dw) {
+    if (!workspace) return fail(HMM_ERR_NULL_POINTER, "workspace is NULL");
+    int32_t* offsets = at<int32_t>(workspace, w.total);
+    Stage stage("linear_fp8_block_dw", st);
+    hipError_t e = hmm::launch_dense_offsets(offsets, T, st);
+    if (e != hipSuccess) return hip_fail(e, "offsets launch");
+    const hmm::DwJob job{offsets, nullptr, 1, (const uint16_t*)x, (const uint16_t*)dy, T, T, H, N, (uint16_t*)dw};
+    e = hmm::launch_dw_dense(job, ((H + 255) / 256) * ((N + 255) / 256) < 64, st);
+    if (e != hipSuccess) return hip_fail(e, "weight gradient launch");
+  }
+  return HMM_OK;
+}
+
+}  // extern "C"
+
 // ------------------------------------------------------------- no-allocation forward
 // hmm_forward_noalloc takes its workspace from this file-scope device array:
 // one copy per device, held from the library's load on that device until the

@@ -1,0 +1,418 @@
+// The E4M3 product with one scale per token and 128 deep group and one per 128 x 128
+// block of the weight:
+//
+//   y[t,n] = sum_g xs[t,g] ws[n/128,g] sum_{k in g} xq[t,k] wq[n,k]
+//
+// Both operands are stored with the contraction contiguous.  A block is 128 x 128 both
+// ways, so the codes of W [H,N] transposed serve the forward and, as they are, the
+// gradient dx = dy W^T with the same scales.  Each group's sums start from zero, are
+// scaled once by xs ws in float32 and added in group order.
+//
+// In every kernel the weight is the matrix instruction's first operand (its rows are
+// the output's columns) and the tokens the second, so that a lane of the accumulator
+// holds ONE token and several output columns: a token's scale is then one register of
+// the lane, and a block's a scalar.
+#include "gemm_common.h"
+#include "kernels.h"
+#include "quant_core.h"
+
+namespace hmm {
+namespace {
+
+constexpr int G = 128;  // group and block size
+
+// ------------------------------------------------------------ weight quantiser
+// One workgroup per block: every thread keeps 8 rows of an 8-column chunk, the maximum
+// crosses the workgroup once, and the codes go out as they are and, through LDS, transposed.
+constexpr int QB_THREADS = 256;
+constexpr int QB_PITCH = G + 8;
+
+__global__ void __launch_bounds__(QB_THREADS) quant_block(const uint16_t* __restrict__ w, int64_t H, int64_t N, int hbs,
+                                                          int nbs, uint8_t* __restrict__ qt, uint8_t* __restrict__ q,
+                                                          float* __restrict__ ds) {
+  __shared__ __attribute__((aligned(16))) uint8_t tile[G * QB_PITCH];
+  __shared__ float wmax[QB_THREADS / 64];
+  const int64_t b = blockIdx.x;
+  const int nb = (int)(b % nbs), hb = (int)(b / nbs % hbs);
+  const int64_t e = b / nbs / hbs;
+  const int c = threadIdx.x & 15, r = threadIdx.x >> 4;  // column chunk, group of 8 rows
+  const int64_t n = (int64_t)nb * G + c * 8, h = (int64_t)hb * G + r * 8;
+  const bool in = n < N;
+  u32x4 raw[8];
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    raw[i] = in ? *reinterpret_cast<const u32x4*>(w + (e * H + h + i) * N + n) : u32x4{0, 0, 0, 0};
+    float v[8];
+    unpack8(raw[i], v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(v[j]));
+  }
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor(m, d));
+  if ((threadIdx.x & 63) == 0) wmax[threadIdx.x >> 6] = m;
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < QB_THREADS / 64; ++k) m = fmaxf(m, wmax[k]);
+  const float sc = scale_of(m);
+  if (threadIdx.x == 0) ds[(e * nbs + nb) * hbs + hb] = 1.f / sc;
+  float s[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) s[j] = sc;
+  uint2 code[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float v[8];
+    unpack8(raw[i], v);
+    code[i] = to_e4m3x8(v, s);
+    if (q && in) *reinterpret_cast<uint2*>(q + (e * H + h + i) * N + n) = code[i];
+  }
+  if (!qt) return;  // the same for every thread
+  // 8 x 8 bytes transposed in registers: column j's 8 rows become 8 bytes
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    uint2 col;
+    const int sh = 8 * (j & 3);
+    uint32_t x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = ((j < 4 ? code[i].x : code[i].y) >> sh) & 0xffu;
+    col.x = x[0] | x[1] << 8 | x[2] << 16 | x[3] << 24;
+    col.y = x[4] | x[5] << 8 | x[6] << 16 | x[7] << 24;
+    *reinterpret_cast<uint2*>(tile + (c * 8 + j) * QB_PITCH + r * 8) = col;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < G * G / 8 / QB_THREADS; ++k) {
+    const int i = threadIdx.x + k * QB_THREADS;
+    const int row = i / (G / 8), ch = i % (G / 8);
+    const int64_t on = (int64_t)nb * G + row;
+    if (on < N)
+      *reinterpret_cast<uint2*>(qt + (e * N + on) * H + (int64_t)hb * G + ch * 8) =
+          *reinterpret_cast<const uint2*>(tile + row * QB_PITCH + ch * 8);
+  }
+}
+
+// ------------------------------------------------------------------- few rows
+// T <= 64: bound by the weight's bytes.  A workgroup owns 16 SUB columns; its 8 waves
+// take the groups in turn, streaming codes from global memory into registers.  The
+// tokens are read in bf16 and quantised in registers (a group of a token is held by the
+// four lanes that share it), which gives exactly the codes of the row quantiser.  Codes
+// of both operands become bf16 (exact) for the 16x16x32 instruction, whose products are
+// exact and whose sums are float32.
+constexpr int RW = 8;
+
+template <int SUB, int NT>
+__global__ void __launch_bounds__(RW * 64) block_rows(const uint16_t* __restrict__ x, const uint8_t* __restrict__ wq,
+                                                      const float* __restrict__ ws, int T, int64_t H, int64_t N,
+                                                      uint16_t* __restrict__ y) {
+  constexpr int COLS = 16 * SUB, LD = COLS + 4;
+  __shared__ float part[RW][16][LD];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int row = lane & 15, quad = lane >> 4;
+  const int64_t n0 = (int64_t)blockIdx.x * COLS;
+  const int groups = (int)(H / G);
+  const uint8_t* wp[SUB];
+#pragma unroll
+  for (int c = 0; c < SUB; ++c) wp[c] = wq + min(n0 + 16 * c + row, N - 1) * H + 32 * quad;
+  const uint16_t* xp[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) xp[n] = x + (int64_t)min(n * 16 + row, T - 1) * H + 32 * quad;
+  const float* wsp = ws + (n0 / G) * groups;
+  f32x4 acc[SUB][NT];
+#pragma unroll
+  for (int c = 0; c < SUB; ++c)
+#pragma unroll
+    for (int n = 0; n < NT; ++n) acc[c][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  u32x4 w[SUB][2], b[NT][4];
+  auto load = [&](int g, u32x4 (&wr)[SUB][2], u32x4 (&br)[NT][4]) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) br[n][q] = *reinterpret_cast<const u32x4*>(xp[n] + (int64_t)g * G + 8 * q);
+#pragma unroll
+    for (int c = 0; c < SUB; ++c)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) wr[c][i] = *reinterpret_cast<const u32x4*>(wp[c] + (int64_t)g * G + 16 * i);
+  };
+  if (wave < groups) load(wave, w, b);
+  for (int g = wave; g < groups; g += RW) {
+    u32x4 wn[SUB][2], bn[NT][4];
+    if (g + RW < groups) load(g + RW, wn, bn);
+    const float sw = wsp[g];
+    // tokens: maximum of the group over this lane's 32 elements and the other three quads
+    float sx[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      float m = 0.f;
+      float v[4][8];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        unpack8(b[n][q], v[q]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(v[q][j]));
+      }
+      m = fmaxf(m, __shfl_xor(m, 16));
+      m = fmaxf(m, __shfl_xor(m, 32));
+      const float sc = scale_of(m);
+      sx[n] = sw * (1.f / sc);
+      float s[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[j] = sc;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint2 code = to_e4m3x8(v[q], s);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          b[n][q][i] = __builtin_bit_cast(
+              uint32_t, i & 1 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(i < 2 ? code.x : code.y, 1.0f, true)
+                              : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(i < 2 ? code.x : code.y, 1.0f, false));
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < SUB; ++c) {
+      u32x4 a[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t v = w[c][q >> 1][2 * (q & 1) + i];
+          a[q][2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v, 1.0f, false));
+          a[q][2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v, 1.0f, true));
+        }
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        f32x4 t = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a[q]), __builtin_bit_cast(bf16x8, b[n][q]),
+                                                      t, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[c][n][i] = __builtin_fmaf(sx[n], t[i], acc[c][n][i]);
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < SUB; ++c)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) w[c][i] = wn[c][i];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) b[n][q] = bn[n][q];
+  }
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    if (n) __syncthreads();
+#pragma unroll
+    for (int c = 0; c < SUB; ++c) *reinterpret_cast<f32x4*>(&part[wave][row][16 * c + 4 * quad]) = acc[c][n];
+    __syncthreads();
+    for (int i = threadIdx.x; i < 16 * COLS; i += RW * 64) {
+      const int t = n * 16 + i / COLS, col = i % COLS;
+      if (t >= T || n0 + col >= N) continue;
+      float s = 0.f;
+#pragma unroll
+      for (int q = 0; q < RW; ++q) s += part[q][i / COLS][col];
+      y[(int64_t)t * N + n0 + col] = f2bf(s);
+    }
+  }
+}
+
+// ------------------------------------------------------------------- many rows
+// BM tokens by BN columns a workgroup, one group of 128 a step, two stages of LDS filled
+// by loads that bypass the registers.  A row of a stage is 128 bytes; its 16-byte chunk c
+// sits at position c ^ (row % 8), so the 16-byte reads of 8 consecutive rows cover every
+// bank once.  (The loads write LDS in lane order, so the permutation is applied to the
+// global address, inside one 128-byte line.)
+template <int BM_, int BN_, int WM_, int WN_>
+struct BlockTile {
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NTHR = WM * WN * 64;
+  static constexpr int TM = BM / WM, TN = BN / WN, MB = TM / 32, NB = TN / 32;
+  static constexpr int STAGE = (BM + BN) * G;
+  static constexpr int LDO = BN + 8;  // output tile pitch, elements
+  static constexpr int LDS = 2 * STAGE > BM * LDO * 2 ? 2 * STAGE : BM * LDO * 2;
+  static_assert(TN <= G && G % TN == 0, "a wave's columns lie in one weight block");
+  static_assert(BM * 8 % NTHR == 0 && BN * 8 % NTHR == 0, "stage loads");
+};
+
+typedef __attribute__((address_space(3))) void lds_void;
+
+struct BlockArgs {
+  const uint8_t *xq, *wq;
+  const float *xs, *ws;
+  int64_t T, H, N;
+  int ws_n, ws_g;  // steps of ws from one column block and from one group to the next
+  uint16_t* y;
+  int mt, nt;
+};
+
+template <int ROWS, int NTHR>
+__device__ __forceinline__ void stage_rows(rsrc_t r, uint8_t* lds, uint32_t pitch, uint32_t koff) {
+  const int tid = threadIdx.x;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+#pragma unroll
+  for (int i = 0; i < ROWS * 8 / NTHR; ++i) {
+    const int row = (i * NTHR + tid) >> 3, pos = tid & 7;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(lds + (i * NTHR + wave * 64) * 16), 16,
+                                             (int)((uint32_t)row * pitch + (uint32_t)((pos ^ (row & 7)) * 16)), (int)koff, 0, 0);
+  }
+}
+
+__device__ __forceinline__ i32x8 frag(const uint8_t* base, int row, int kk, int half) {
+  const int c = 4 * kk + half;
+  const u32x4 lo = *reinterpret_cast<const u32x4*>(base + row * G + ((c ^ (row & 7)) * 16));
+  const u32x4 hi = *reinterpret_cast<const u32x4*>(base + row * G + (((c + 2) ^ (row & 7)) * 16));
+  return i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+}
+
+template <class C>
+__global__ void __launch_bounds__(C::NTHR) block_gemm(const BlockArgs A) {
+  __shared__ __attribute__((aligned(128))) uint8_t smem[C::LDS];
+  const int nblocks = gridDim.x;
+  int mt, nt;
+  const int logical = xcd_remap(blockIdx.x, nblocks);
+  if (logical >= A.mt * A.nt) return;
+  raster(logical, A.mt, A.nt, mt, nt);
+  const int64_t m0 = (int64_t)mt * C::BM, n0 = (int64_t)nt * C::BN;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int wm = wave / C::WN, wn = wave % C::WN;
+  const int half = lane >> 5, l32 = lane & 31;
+  const uint32_t pitch = (uint32_t)A.H;
+  const rsrc_t rx = make_rsrc(A.xq + m0 * A.H, min((int64_t)C::BM, A.T - m0) * A.H);
+  const rsrc_t rw = make_rsrc(A.wq + n0 * A.H, min((int64_t)C::BN, A.N - n0) * A.H);
+  const int groups = (int)(A.H / G);
+  const float* xsp[C::MB];
+#pragma unroll
+  for (int mb = 0; mb < C::MB; ++mb) xsp[mb] = A.xs + min(m0 + wm * C::TM + mb * 32 + l32, A.T - 1) * groups;
+  const float* wsp = A.ws + ((n0 + wn * C::TN) / G < (A.N + G - 1) / G ? (n0 + wn * C::TN) / G : 0) * A.ws_n;
+
+  f32x16 acc[C::NB][C::MB];
+#pragma unroll
+  for (int nb = 0; nb < C::NB; ++nb)
+#pragma unroll
+    for (int mb = 0; mb < C::MB; ++mb)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[nb][mb][r] = 0.f;
+
+  auto stage = [&](int g, int buf) {
+    uint8_t* s = smem + buf * C::STAGE;
+    stage_rows<C::BN, C::NTHR>(rw, s, pitch, (uint32_t)g * G);
+    stage_rows<C::BM, C::NTHR>(rx, s + C::BN * G, pitch, (uint32_t)g * G);
+  };
+  float xs[C::MB];
+#pragma unroll
+  for (int mb = 0; mb < C::MB; ++mb) xs[mb] = xsp[mb][0];
+  stage(0, 0);
+  for (int g = 0; g < groups; ++g) {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();  // stage g has landed for every wave, and every wave is done with stage g - 1
+    const float sw = wsp[(int64_t)g * A.ws_g];
+    float s[C::MB];
+#pragma unroll
+    for (int mb = 0; mb < C::MB; ++mb) s[mb] = xs[mb] * sw;
+    if (g + 1 < groups) {
+      stage(g + 1, (g + 1) & 1);
+#pragma unroll
+      for (int mb = 0; mb < C::MB; ++mb) xs[mb] = xsp[mb][g + 1];
+    }
+    const uint8_t* sw_ = smem + (g & 1) * C::STAGE;
+    const uint8_t* sx_ = sw_ + C::BN * G;
+    i32x8 fb[C::MB][2];
+#pragma unroll
+    for (int mb = 0; mb < C::MB; ++mb)
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk) fb[mb][kk] = frag(sx_, wm * C::TM + mb * 32 + l32, kk, half);
+#pragma unroll
+    for (int nb = 0; nb < C::NB; ++nb) {
+      const i32x8 a0 = frag(sw_, wn * C::TN + nb * 32 + l32, 0, half);
+      const i32x8 a1 = frag(sw_, wn * C::TN + nb * 32 + l32, 1, half);
+#pragma unroll
+      for (int mb = 0; mb < C::MB; ++mb) {
+        f32x16 t = {};
+        t = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a0, fb[mb][0], t, 0, 0, 0, 127, 0, 127);
+        t = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a1, fb[mb][1], t, 0, 0, 0, 127, 0, 127);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[nb][mb][r] = __builtin_fmaf(s[mb], t[r], acc[nb][mb][r]);
+      }
+    }
+  }
+  __syncthreads();
+  // the tile in bf16 through LDS, so that stores are rows of 16-byte chunks
+  uint16_t* out = reinterpret_cast<uint16_t*>(smem);
+#pragma unroll
+  for (int nb = 0; nb < C::NB; ++nb)
+#pragma unroll
+    for (int mb = 0; mb < C::MB; ++mb)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        uint2 v;
+        v.x = (uint32_t)f2bf(acc[nb][mb][4 * q]) | ((uint32_t)f2bf(acc[nb][mb][4 * q + 1]) << 16);
+        v.y = (uint32_t)f2bf(acc[nb][mb][4 * q + 2]) | ((uint32_t)f2bf(acc[nb][mb][4 * q + 3]) << 16);
+        *reinterpret_cast<uint2*>(out + (wm * C::TM + mb * 32 + l32) * C::LDO + wn * C::TN + nb * 32 + 8 * q + 4 * half) = v;
+      }
+  __syncthreads();
+  constexpr int CPR = C::BN / 8;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < C::BM * CPR; i += C::NTHR) {
+    const int r = i / CPR, c = i % CPR * 8;
+    if (m0 + r < A.T && n0 + c < A.N)
+      store16_stream(A.y + (m0 + r) * A.N + n0 + c, *reinterpret_cast<const u32x4*>(out + r * C::LDO + c));
+  }
+}
+
+template <class C>
+hipError_t launch_gemm(BlockArgs a, hipStream_t stream) {
+  a.mt = (int)((a.T + C::BM - 1) / C::BM);
+  a.nt = (int)((a.N + C::BN - 1) / C::BN);
+  const int64_t blocks = ((int64_t)a.mt * a.nt + 7) / 8 * 8;
+  if (blocks > 0x7fffffff) return hipErrorInvalidValue;
+  block_gemm<C><<<(unsigned)blocks, C::NTHR, 0, stream>>>(a);
+  return hipGetLastError();
+}
+
+template <int NT>
+hipError_t launch_rows(const uint16_t* x, const uint8_t* wq, const float* ws, int T, int64_t H, int64_t N, uint16_t* y,
+                       hipStream_t stream) {
+  block_rows<1, NT><<<(unsigned)((N + 15) / 16), RW * 64, 0, stream>>>(x, wq, ws, T, H, N, y);
+  return hipGetLastError();
+}
+
+__global__ void dense_offsets(int32_t* offsets, int32_t T) {
+  offsets[0] = 0;
+  offsets[1] = T;
+}
+
+}  // namespace
+
+hipError_t launch_quant_block(const uint16_t* w, int64_t E, int64_t H, int64_t N, uint8_t* qt, uint8_t* q, float* ds,
+                              hipStream_t stream) {
+  const int64_t hbs = H / G, nbs = (N + G - 1) / G;
+  if (E * hbs * nbs > 0x7fffffff) return hipErrorInvalidValue;
+  quant_block<<<(unsigned)(E * hbs * nbs), QB_THREADS, 0, stream>>>(w, H, N, (int)hbs, (int)nbs, qt, q, ds);
+  return hipGetLastError();
+}
+
+hipError_t launch_block_rows(const uint16_t* x, const uint8_t* wq, const float* ws, int T, int64_t H, int64_t N, uint16_t* y,
+                             hipStream_t stream) {
+  if (T <= 16) return launch_rows<1>(x, wq, ws, T, H, N, y, stream);
+  if (T <= 32) return launch_rows<2>(x, wq, ws, T, H, N, y, stream);
+  return launch_rows<4>(x, wq, ws, T, H, N, y, stream);
+}
+
+hipError_t launch_block_gemm(const uint8_t* xq, const float* xs, const uint8_t* wq, const float* ws, int64_t T, int64_t H,
+                             int64_t N, bool ws_transposed, uint16_t* y, hipStream_t stream) {
+  const int groups = (int)(H / G), nbs = (int)((N + G - 1) / G);
+  const BlockArgs a{xq, wq, xs, ws, T, H, N, ws_transposed ? 1 : groups, ws_transposed ? nbs : 1, y, 0, 0};
+  const auto tiles = [&](int64_t bm, int64_t bn) { return ((T + bm - 1) / bm) * ((N + bn - 1) / bn); };
+  if (tiles(256, 256) >= 192) return launch_gemm<BlockTile<256, 256, 4, 2>>(a, stream);
+  if (tiles(128, 128) >= 192) return launch_gemm<BlockTile<128, 128, 2, 2>>(a, stream);
+  return launch_gemm<BlockTile<64, 64, 2, 2>>(a, stream);
+}
+
+hipError_t launch_dense_offsets(int32_t* offsets, int64_t T, hipStream_t stream) {
+  dense_offsets<<<1, 1, 0, stream>>>(offsets, (int32_t)T);
+  return hipGetLastError();
+}
+
+}  // namespace hmm

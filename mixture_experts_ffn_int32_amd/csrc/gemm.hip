@@ -341,6 +341,11 @@ hipError_t launch_dw2(const DwJob* jobs, int n, bool narrow, hipStream_t stream)
                 : launch_dw_jobs<Big, false, true>(jobs, n, stream);
 }
 
+hipError_t launch_dw_dense(const DwJob& job, bool narrow, hipStream_t stream) {
+  return narrow ? launch_dw_jobs<Narrow, false, false>(&job, 1, stream)
+                : launch_dw_jobs<Big, false, false>(&job, 1, stream);
+}
+
 hipError_t launch_act_grad_dw2_narrow(const ActGradJob* ag, const DwJob* dw2, int n, hipStream_t stream) {
   typedef ActGrad<Narrow, true> P1;
   typedef Dw<Narrow, false, true> P2;

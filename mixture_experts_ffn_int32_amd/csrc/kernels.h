@@ -174,6 +174,8 @@ hipError_t launch_dw1(const DwJob* jobs, int n, bool narrow, hipStream_t stream)
 // for the weight gradients to start the longest reductions first (route.hip)
 hipError_t launch_expert_order(const int32_t* counts, int E, int32_t* order, hipStream_t stream);
 hipError_t launch_dw2(const DwJob* jobs, int n, bool narrow, hipStream_t stream);
+// C = A^T B of plain matrices (E = 1, offsets = {0, rows}; tok_of_row is not read)
+hipError_t launch_dw_dense(const DwJob& job, bool narrow, hipStream_t stream);
 // Small problems (narrow tiles): the independent products share a launch,
 // act_grad with W2Grad, then input_grad with W1Grad (the same products as above;
 // with a shared expert, its two products join each launch).
@@ -317,5 +319,42 @@ struct NormSums {
 int64_t norm_partial_rows(int64_t T, int64_t H);
 hipError_t launch_residual_norm(const NormArgs& A, hipStream_t stream);
 hipError_t launch_residual_norm_bwd(const NormArgs& A, const NormGradArgs& G, hipStream_t stream);
+
+// The layer for a few tokens (decode.hip).
+constexpr int DECODE_MAX_TOKENS = 64;
+struct DecodeArgs {
+  int T, E, K;
+  int64_t H, I;
+  int wbytes;               // bytes per weight element: 2 (bf16) or 1 (E4M3)
+  const uint16_t* x;        // [T][H]
+  const int32_t* ids;       // [T][K]; ids outside [0, E) are dropped
+  const float* weights;     // [T][K]
+  const void* up;           // bf16 [E][H][2I], or E4M3 [E][2I][H]
+  const void* down;         // bf16 [E][I][H], or E4M3 [E][H][I]
+  const float* up_descale;  // E4M3: [E][2I/128][H/128]
+  const float* down_descale;// E4M3: [E][H/128][I/128]
+  uint16_t* a;              // [T K][2I]: hi | lo
+  float* o;                 // [T K][H]
+  uint32_t* count;          // [col_tiles]
+  int col_tiles;
+  uint16_t* y;              // [T][H]
+};
+int decode_col_tiles(int64_t H, bool fp8);
+hipError_t launch_router(const uint16_t* x, const void* wr, bool wr_f32, int T, int64_t H, int E, int K, bool renorm,
+                         double* logits, int32_t* ids, float* weights, hipStream_t stream);
+hipError_t launch_moe_decode(const DecodeArgs& A, bool fp8, hipStream_t stream);
+
+// The E4M3 product with 128 x 128 block scales (fp8_block.hip).  H is a multiple of 128, N of 16.
+//   w [E][H][N] bf16 -> qt [E][N][H] and / or q [E][H][N] (NULL: not written), ds [E][ceil(N/128)][H/128]
+hipError_t launch_quant_block(const uint16_t* w, int64_t E, int64_t H, int64_t N, uint8_t* qt, uint8_t* q, float* ds,
+                              hipStream_t stream);
+constexpr int BLOCK_MAX_ROWS = 64;  // tokens up to which launch_block_rows takes them
+//   y [T][N] of bf16 tokens x [T][H], quantised on the way (T <= BLOCK_MAX_ROWS)
+hipError_t launch_block_rows(const uint16_t* x, const uint8_t* wq, const float* ws, int T, int64_t H, int64_t N, uint16_t* y,
+                             hipStream_t stream);
+//   y [T][N] of codes xq [T][H], xs [T][H/128]; ws [ceil(N/128)][H/128], or its transpose
+hipError_t launch_block_gemm(const uint8_t* xq, const float* xs, const uint8_t* wq, const float* ws, int64_t T, int64_t H,
+                             int64_t N, bool ws_transposed, uint16_t* y, hipStream_t stream);
+hipError_t launch_dense_offsets(int32_t* offsets, int64_t T, hipStream_t stream);
 
 }  // namespace hmm

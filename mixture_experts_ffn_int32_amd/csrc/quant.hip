@@ -13,29 +13,12 @@
 // more than a rounding of the product, which still converts to 448).
 #include "device.h"
 #include "kernels.h"
+#include "quant_core.h"
 
 namespace hmm {
 
 constexpr int QT = 256;  // threads per quantisation block
 constexpr int QH = 256;  // hidden rows per column-maximum chunk
-
-// 448 / max|x| in float32; an all-zero row or group gets 1.  Below a largest
-// value of about 1.3e-36 (bf16 holds values down to ~9e-41) the quotient
-// overflows: it is clamped to the largest finite float32, so the codes stay
-// finite (x * scale is then at most ~448) and the descale 1 / scale is a
-// subnormal float32 (about 2.9e-39) instead of 0.
-__device__ __forceinline__ float scale_of(float absmax) {
-  return absmax > 0.f ? fminf(448.f / absmax, 3.40282347e38f) : 1.f;
-}
-
-// 8 floats * scale -> 8 E4M3 bytes
-__device__ __forceinline__ uint2 to_e4m3x8(const float (&v)[8], const float (&s)[8]) {
-  int lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[0] * s[0], v[1] * s[1], 0, false);
-  lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[2] * s[2], v[3] * s[3], lo, true);
-  int hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[4] * s[4], v[5] * s[5], 0, false);
-  hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[6] * s[6], v[7] * s[7], hi, true);
-  return make_uint2((unsigned)lo, (unsigned)hi);
-}
 
 // One block per token row: xq[t] = e4m3(x[t] * scale), dsx[t] = 1 / scale.
 __global__ void __launch_bounds__(QT) quant_rows_fp8(const uint16_t* __restrict__ x, int64_t H,

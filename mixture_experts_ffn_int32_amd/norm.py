@@ -11,7 +11,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _lib
-from .moe import _contig, _ptr, _stream
+from .moe import _aligned, _ptr, _stream
 
 _MAX_H = 16384
 _DTYPES = {torch.bfloat16: _lib.HMM_BF16, torch.float32: _lib.HMM_F32}
@@ -70,10 +70,10 @@ class ResidualNormFunction(torch.autograd.Function):
         kind = _gate_kind(gate, T, H)
         wt = norm_weight.dtype
         prob = _lib.NormProblem(T, H, _DTYPES[residual.dtype], _DTYPES[wt], kind, eps, scale)
-        r, w = _contig(residual), _contig(norm_weight)
-        y_ = None if y is None else _contig(y)
-        wp = None if post_weight is None else _contig(post_weight)
-        g = None if gate is None else _contig(gate)
+        r, w = _aligned(residual), _aligned(norm_weight)
+        y_ = None if y is None else _aligned(y)
+        wp = None if post_weight is None else _aligned(post_weight)
+        g = None if gate is None else _aligned(gate)
         dev = r.device
         grad = any(ctx.needs_input_grad)
         with torch.cuda.device(dev):
@@ -98,8 +98,8 @@ class ResidualNormFunction(torch.autograd.Function):
         if d_out is None and d_normed is None:
             return (None,) * 7
         dev = r.device
-        d_out = None if d_out is None else _contig(d_out, r.dtype)
-        d_normed = None if d_normed is None else _contig(d_normed, torch.bfloat16)
+        d_out = None if d_out is None else _aligned(d_out, r.dtype)
+        d_normed = None if d_normed is None else _aligned(d_normed, torch.bfloat16)
         with torch.cuda.device(dev):
             lib = _lib.load()
             dy = None if y is None else torch.empty_like(y)

@@ -1,4 +1,5 @@
-"""Float64 references of the operators around the experts: the norms of a block.
+"""Float64 references of the operators around the experts: the norms of a block, the E4M3
+product with 128 x 128 block scales, and the layer for a few tokens.
 
 Plain numpy, written from the formulas, sharing no code with the HIP path.  Each
 gradient comes with the sum of the absolute terms it is made of, the scale that
@@ -6,6 +7,10 @@ float32 rounding errors are measured on.
 """
 
 import numpy as np
+
+from .quant import quantize_rows
+
+GROUP = 128
 
 
 def rms(v, eps):
@@ -52,3 +57,78 @@ def residual_norm_grads(tr, dn, y, rs, w, wp, gate, scale, eps):
         else:
             out["d_gate"] = (dg.sum(axis=1, keepdims=True), dga.sum(axis=1, keepdims=True))
     return out
+
+
+def e4m3_values(codes):
+    """E4M3 bytes as the values they stand for (OCP e4m3fn: bias 7, no infinity, 0x7f is NaN)."""
+    c = np.asarray(codes, np.uint8).astype(np.int64)
+    e, m = (c >> 3) & 15, c & 7
+    v = np.where(e == 0, m * 2.0 ** -9, (8 + m) * 2.0 ** (e - 10.0))
+    v = np.where((c & 127) == 127, np.nan, v)
+    return np.where(c >> 7, -v, v)
+
+
+def quantize_block(w):
+    """(E4M3 values [N,H], float32 descales [ceil(N/128), H/128]) of w [H,N]: one row of quantize_rows per block."""
+    H, N = w.shape
+    nb, hb = (N + GROUP - 1) // GROUP, H // GROUP
+    t = np.zeros((nb * GROUP, H), np.float32)
+    t[:N] = np.asarray(w, np.float32).T
+    blocks = t.reshape(nb, GROUP, hb, GROUP).transpose(0, 2, 1, 3).reshape(nb * hb, GROUP * GROUP)
+    q, _, d = quantize_rows(blocks)
+    q = np.asarray(q, np.float64).reshape(nb, hb, GROUP, GROUP).transpose(0, 2, 1, 3).reshape(nb * GROUP, H)[:N]
+    return q, np.asarray(d, np.float32).reshape(nb, hb)
+
+
+def block_product(xv, xs, wv, ws):
+    """y of token values xv [T,H] and descales xs [T,H/128], weight values wv [N,H] and block descales ws.
+
+    Returns (y, largest |x| times largest |w| of each group with its scales, summed; sum of absolute scaled groups)."""
+    T, H = xv.shape
+    N = wv.shape[0]
+    y, big, sabs = (np.zeros((T, N)) for _ in range(3))
+    rep = np.arange(N) // GROUP
+    for g in range(H // GROUP):
+        k = slice(g * GROUP, (g + 1) * GROUP)
+        s = xs[:, g].astype(np.float64)[:, None] * ws[rep, g].astype(np.float64)[None]
+        p = xv[:, k] @ wv[:, k].T
+        y += s * p
+        sabs += np.abs(s * p)
+        big += s * np.abs(xv[:, k]).max(axis=1)[:, None] * np.abs(wv[:, k]).max(axis=1)[None]
+    return y, big, sabs
+
+
+def route(x, wr, K, renormalize):
+    """The K largest logits of each token (ties to the lower expert) and their softmax weights."""
+    logits = x @ wr.T
+    ids = np.argsort(-logits, axis=1, kind="stable")[:, :K]
+    e = np.exp(logits - logits.max(axis=1, keepdims=True))
+    p = np.take_along_axis(e, ids, axis=1)
+    return ids.astype(np.int32), p / (p if renormalize else e).sum(axis=1, keepdims=True)
+
+
+def moe(x, ids, weights, up, down, eh, ea, eo):
+    """y of the layer for a few tokens and the bound of its float32 error before y's rounding.
+
+    up(e) [H,2I] and down(e) [I,H] give an expert's matrices.  eh: relative error of the up-projection's sums
+    (of the sum of absolute products), ea: of a, eo: of the down-projection's and the weighted sums."""
+    T, K = ids.shape
+    y = np.zeros_like(x)
+    dev = np.zeros_like(x)
+    for t in range(T):
+        for k in range(K):
+            e = ids[t, k]
+            try:
+                W1, W2 = up(e), down(e)
+            except IndexError:
+                continue
+            I = W2.shape[0]
+            h, ha = x[t] @ W1, eh * (np.abs(x[t]) @ np.abs(W1))
+            g, u, dg, du = h[:I], h[I:], ha[:I], ha[I:]
+            s = 1.0 / (1.0 + np.exp(-g))
+            a = g * s * u
+            # |d silu| <= 1.1; second order terms are far below the bound's slack
+            da = 1.1 * dg * np.abs(u) + np.abs(g * s) * du + ea * np.abs(a)
+            y[t] += weights[t, k] * (a @ W2)
+            dev[t] += np.abs(weights[t, k]) * (da @ np.abs(W2) + eo * (np.abs(a) @ np.abs(W2)))
+    return y, dev
