@@ -461,18 +461,24 @@ hmm_status hmm_moe_decode(const hmm_decode_problem* p, const void* x, const void
 
 /* The E4M3 product with one scale per token and group of 128 and one per 128 x 128
  * block of the weight (a dense projection; the experts of hmm_moe_decode take the same
- * weights).  With (xq, xs) from hmm_quant_rows_group and (codes_t, descale) from
+ * weights).  With (xq, xs) from hmm_quant_rows_block and (codes_t, descale) from
  * hmm_quant_block:
  *   y[t,n] = sum_g xs[t,g] descale[n/128,g] sum_{k in g} xq[t,k] codes_t[n,k]
  * Each group's sums are taken by the matrix instruction, scaled in float32 and added in
  * group order; y is bf16, rounded once.
  *
+ * The rule of both quantisers, per group or block: scale = 448 * (1 / max|v|), the
+ * reciprocal and the product each rounded to float32 (1 for an all-zero one, at most the
+ * largest finite float32); code = round-to-nearest-even E4M3 of v * scale; descale =
+ * 1 / scale.  (hmm_quant_rows_group divides 448 by the maximum instead: its scale may
+ * differ in the last bit; hmm_matmul_fp8_block takes its codes and descales as well.)
+ * hmm_quant_rows_block: x bf16 [T,H], H a multiple of 128 in [128, 262144], per token and
+ *   group of 128 -> xq [T,H] E4M3 bytes, xs [T,H/128] float32.
  * hmm_quant_block: w bf16 [E,H,N], per (expert, block of 128 rows, block of 128 columns;
- *   a last block of columns may be narrower) the rule of hmm_quant_rows_group: codes_t
- *   [E,N,H] and / or codes [E,H,N] E4M3 bytes (NULL: not written; one at least),
- *   descale [E,ceil(N/128),H/128] float32.
+ *   a last block of columns may be narrower): codes_t [E,N,H] and / or codes [E,H,N] E4M3
+ *   bytes (NULL: not written; one at least), descale [E,ceil(N/128),H/128] float32.
  * hmm_matmul_fp8_block: the product of codes.
- * hmm_linear_fp8_block: x bf16 [T,H] quantised by the rule of hmm_quant_rows_group, then
+ * hmm_linear_fp8_block: x bf16 [T,H] quantised as hmm_quant_rows_block does, then
  *   the product; for T <= 64 in one launch without workspace (forward_bytes is 0 then).
  * hmm_linear_fp8_block_grad: of dy bf16 [T,N],
  *   dx bf16 [T,H]: dy quantised per token and 128 of N, times the same codes (in the
@@ -484,6 +490,7 @@ hmm_status hmm_moe_decode(const hmm_decode_problem* p, const void* x, const void
  * gradient of 128.  dw needs x and dy below 4 GiB each (else HMM_ERR_UNSUPPORTED). */
 hmm_status hmm_quant_block(const void* w, int64_t E, int64_t H, int64_t N, uint8_t* codes_t, uint8_t* codes, float* descale,
                            void* stream);
+hmm_status hmm_quant_rows_block(const void* x, int64_t T, int64_t H, uint8_t* xq, float* xs, void* stream);
 hmm_status hmm_matmul_fp8_block(const uint8_t* xq, const float* xs, const uint8_t* codes_t, const float* descale, int64_t T,
                                 int64_t H, int64_t N, void* y, void* stream);
 hmm_status hmm_linear_fp8_block_sizes(int64_t T, int64_t H, int64_t N, size_t* forward_bytes, size_t* grad_bytes);

@@ -42,7 +42,7 @@ EXPORTS = (
     "hmm_quant_cols_fp8", "hmm_forward_shared", "hmm_backward_shared", "hmm_quant_rows_mx", "hmm_quant_cols_mx",
     "hmm_quant_rows_group", "hmm_quant_cols_group", "hmm_set_fused_spin_limit", "hmm_forward_noalloc",
     "hmm_residual_norm", "hmm_residual_norm_backward_sizes", "hmm_residual_norm_backward",
-    "hmm_moe_decode_sizes", "hmm_moe_decode", "hmm_quant_block", "hmm_matmul_fp8_block", "hmm_linear_fp8_block_sizes",
+    "hmm_moe_decode_sizes", "hmm_moe_decode", "hmm_quant_block", "hmm_quant_rows_block", "hmm_matmul_fp8_block", "hmm_linear_fp8_block_sizes",
     "hmm_linear_fp8_block", "hmm_linear_fp8_block_grad",
 )
 
@@ -108,6 +108,7 @@ _SIGS = {
     "hmm_moe_decode_sizes": [_DEC, ctypes.POINTER(_SZ)],
     "hmm_moe_decode": [_DEC] + [_P] * 10 + [_SZ, _P],
     "hmm_quant_block": [_P, _I64, _I64, _I64, _P, _P, _P, _P],
+    "hmm_quant_rows_block": [_P, _I64, _I64, _P, _P, _P],
     "hmm_matmul_fp8_block": [_P, _P, _P, _P, _I64, _I64, _I64, _P, _P],
     "hmm_linear_fp8_block_sizes": [_I64, _I64, _I64, ctypes.POINTER(_SZ), ctypes.POINTER(_SZ)],
     "hmm_linear_fp8_block": [_P, _P, _P, _I64, _I64, _I64, _P, _P, _SZ, _P],

@@ -1461,6 +1461,16 @@ hmm_status hmm_quant_block(const void* w, int64_t E, int64_t H, int64_t N, uint8
   return e == hipSuccess ? HMM_OK : hip_fail(e, "block quantisation launch");
 }
 
+hmm_status hmm_quant_rows_block(const void* x, int64_t T, int64_t H, uint8_t* xq, float* xs, void* stream) {
+  hmm_status s = block_dims(T, 128, H, 128);  // rows of a gradient are as wide as N
+  if (s != HMM_OK) return s;
+  const bool ne = T > 0;
+  if ((s = need(x, ne, "x")) || (s = need(xq, ne, "xq")) || (s = need(xs, ne, "xs"))) return s;
+  Stage stage("quant_rows_block", (hipStream_t)stream);
+  const hipError_t e = hmm::launch_quant_rows_block((const uint16_t*)x, T, H, xq, xs, (hipStream_t)stream);
+  return e == hipSuccess ? HMM_OK : hip_fail(e, "token quantisation launch");
+}
+
 hmm_status hmm_matmul_fp8_block(const uint8_t* xq, const float* xs, const uint8_t* codes_t, const float* descale, int64_t T,
                                 int64_t H, int64_t N, void* y, void* stream) {
   hmm_status s = block_dims(T, H, N, 16);
@@ -1504,7 +1514,7 @@ hmm_status hmm_linear_fp8_block(const void* x, const uint8_t* codes_t, const flo
     return fail(HMM_ERR_WORKSPACE_TOO_SMALL, "workspace is %zu bytes, %zu needed", workspace_bytes, w.total);
   uint8_t* xq = at<uint8_t>(workspace, w.xq);
   float* xs = at<float>(workspace, w.xs);
-  if ((s = hmm_quant_rows_group(x, T, H, xq, xs, stream)) != HMM_OK) return s;
+  if ((s = hmm_quant_rows_block(x, T, H, xq, xs, stream)) != HMM_OK) return s;
   return hmm_matmul_fp8_block(xq, xs, codes_t, descale, T, H, N, y, stream);
 }
 
@@ -1528,7 +1538,7 @@ hmm_status hmm_linear_fp8_block_grad(const void* dy, const void* x, const uint8_
   if (ne && dx) {
     uint8_t* gq = at<uint8_t>(workspace, w.xq);
     float* gs = at<float>(workspace, w.xs);
-    if ((s = hmm_quant_rows_group(dy, T, N, gq, gs, stream)) != HMM_OK) return s;
+    if ((s = hmm_quant_rows_block(dy, T, N, gq, gs, stream)) != HMM_OK) return s;
     Stage stage("matmul_fp8_block_dx", st);
     const hipError_t e = hmm::launch_block_gemm(gq, gs, codes, descale, T, N, H, true, (uint16_t*)dx, st);
     if (e != hipSuccess) return hip_fail(e, "FP8 block product launch");

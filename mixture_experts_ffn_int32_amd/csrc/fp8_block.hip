@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(QB_THREADS) quant_block(const uint16_t* __rest
   __syncthreads();
 #pragma unroll
   for (int k = 0; k < QB_THREADS / 64; ++k) m = fmaxf(m, wmax[k]);
-  const float sc = scale_of(m);
+  const float sc = block_scale_of(m);
   if (threadIdx.x == 0) ds[(e * nbs + nb) * hbs + hb] = 1.f / sc;
   float s[8];
 #pragma unroll
@@ -89,6 +89,30 @@ __global__ void __launch_bounds__(QB_THREADS) quant_block(const uint16_t* __rest
     if (on < N)
       *reinterpret_cast<uint2*>(qt + (e * N + on) * H + (int64_t)hb * G + ch * 8) =
           *reinterpret_cast<const uint2*>(tile + row * QB_PITCH + ch * 8);
+  }
+}
+
+// ------------------------------------------------------------- token quantiser
+// 16 consecutive lanes hold a group (8 elements each); H / 8 is a multiple of 16, so a
+// group's lanes are active together.
+constexpr int QR_THREADS = 256;
+constexpr int64_t QR_MAX_BLOCKS = 1 << 20;
+
+__global__ void __launch_bounds__(QR_THREADS) quant_rows_block(const uint16_t* __restrict__ x, int64_t chunks,
+                                                               uint8_t* __restrict__ xq, float* __restrict__ xs) {
+  for (int64_t c = (int64_t)blockIdx.x * QR_THREADS + threadIdx.x; c < chunks; c += (int64_t)gridDim.x * QR_THREADS) {
+    float v[8], s[8];
+    unpack8(*reinterpret_cast<const u32x4*>(x + c * 8), v);
+    float m = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(v[j]));
+#pragma unroll
+    for (int d = 8; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor(m, d));
+    const float sc = block_scale_of(m);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s[j] = sc;
+    *reinterpret_cast<uint2*>(xq + c * 8) = to_e4m3x8(v, s);
+    if ((c & 15) == 0) xs[c >> 4] = 1.f / sc;
   }
 }
 
@@ -155,7 +179,7 @@ __global__ void __launch_bounds__(RW * 64) block_rows(const uint16_t* __restrict
       }
       m = fmaxf(m, __shfl_xor(m, 16));
       m = fmaxf(m, __shfl_xor(m, 32));
-      const float sc = scale_of(m);
+      const float sc = block_scale_of(m);
       sx[n] = sw * (1.f / sc);
       float s[8];
 #pragma unroll
@@ -390,6 +414,13 @@ hipError_t launch_quant_block(const uint16_t* w, int64_t E, int64_t H, int64_t N
   const int64_t hbs = H / G, nbs = (N + G - 1) / G;
   if (E * hbs * nbs > 0x7fffffff) return hipErrorInvalidValue;
   quant_block<<<(unsigned)(E * hbs * nbs), QB_THREADS, 0, stream>>>(w, H, N, (int)hbs, (int)nbs, qt, q, ds);
+  return hipGetLastError();
+}
+
+hipError_t launch_quant_rows_block(const uint16_t* x, int64_t T, int64_t H, uint8_t* xq, float* xs, hipStream_t stream) {
+  const int64_t chunks = T * (H / 8), blocks = (chunks + QR_THREADS - 1) / QR_THREADS;
+  if (chunks <= 0) return hipSuccess;
+  quant_rows_block<<<(unsigned)(blocks < QR_MAX_BLOCKS ? blocks : QR_MAX_BLOCKS), QR_THREADS, 0, stream>>>(x, chunks, xq, xs);
   return hipGetLastError();
 }
 

@@ -14,6 +14,13 @@ __device__ __forceinline__ float scale_of(float absmax) {
   return absmax > 0.f ? fminf(448.f / absmax, 3.40282347e38f) : 1.f;
 }
 
+// The rule of the 128 x 128 block products (both operands): 448 times the reciprocal of
+// max|x|, each rounded to float32, as tensor code evaluates 448 / max; it may differ from
+// scale_of's quotient in the last bit.  The same clamp (1 / max overflows below 2.9e-39).
+__device__ __forceinline__ float block_scale_of(float absmax) {
+  return absmax > 0.f ? fminf((1.f / absmax) * 448.f, 3.40282347e38f) : 1.f;
+}
+
 // 8 floats * scale -> 8 E4M3 bytes
 __device__ __forceinline__ uint2 to_e4m3x8(const float (&v)[8], const float (&s)[8]) {
   int lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[0] * s[0], v[1] * s[1], 0, false);

@@ -1,5 +1,5 @@
 """Python binding of the E4M3 product with 128 x 128 block scales: ``quantize_block``,
-``matmul_fp8_block`` and the differentiable ``linear_fp8_block``.
+``quantize_rows_block``, ``matmul_fp8_block`` and the differentiable ``linear_fp8_block``.
 
 Argument marshalling only; the kernels are those of csrc/fp8_block.hip behind
 hmm_quant_block, hmm_matmul_fp8_block, hmm_linear_fp8_block and hmm_linear_fp8_block_grad.
@@ -50,8 +50,8 @@ def quantize_block(w):
 
     w bf16 [H,N] or [E,H,N], H a multiple of 128 and N of 16 (a last block of columns may be narrower).
     Returns (codes uint8 [(E,) N, H], descale float32 [(E,) ceil(N/128), H/128]): the codes are transposed, so
-    that the contraction is contiguous.  Per block: scale = 448 / max|block| (1 for zeros), code = E4M3 of w * scale,
-    descale = 1 / scale."""
+    that the contraction is contiguous.  Per block, in float32: scale = 448 * (1 / max|block|) (1 for
+    zeros), code = E4M3 of w * scale, descale = 1 / scale."""
     _tensor("w", w, torch.bfloat16, (2, 3))
     _widths(w.shape[-2], w.shape[-1], 16)
     if w.dim() == 3 and w.shape[0] < 1:
@@ -59,6 +59,20 @@ def quantize_block(w):
     with torch.cuda.device(w.device):
         qt, _, ds = _quant(_aligned(w.detach() if w.dim() == 3 else w.detach()[None]), False)
     return (qt, ds) if w.dim() == 3 else (qt[0], ds[0])
+
+
+def quantize_rows_block(x):
+    """The tokens' side: (codes uint8 [T,H], descale float32 [T,H/128]) of x bf16 [T,H], quantize_block's rule per token
+    and group of 128, as linear_fp8_block applies it."""
+    _tensor("x", x, torch.bfloat16, (2,))
+    T, H = x.shape
+    _widths(GROUP, H, GROUP)
+    x = _aligned(x.detach())
+    q = torch.empty((T, H), dtype=torch.uint8, device=x.device)
+    d = torch.empty((T, H // GROUP), dtype=torch.float32, device=x.device)
+    with torch.cuda.device(x.device):
+        _lib.check(_lib.load().hmm_quant_rows_block(_ptr(x), T, H, _ptr(q), _ptr(d), _stream(x.device)))
+    return q, d
 
 
 def _check_codes(codes, descale, H, device):
@@ -73,7 +87,7 @@ def _check_codes(codes, descale, H, device):
 
 
 def matmul_fp8_block(xq, xs, codes, descale):
-    """y bf16 [T,N] of tokens (xq uint8 [T,H], xs float32 [T,H/128], as quantize_rows_group gives them) and a weight
+    """y bf16 [T,N] of tokens (xq uint8 [T,H], xs float32 [T,H/128], as quantize_rows_block gives them) and a weight
     (codes uint8 [N,H], descale float32 [ceil(N/128),H/128], as quantize_block does)."""
     _tensor("xq", xq, torch.uint8, (2,))
     T, H = xq.shape
@@ -138,7 +152,7 @@ class LinearFp8BlockFunction(torch.autograd.Function):
 def linear_fp8_block(x, weight):
     """y bf16 [T,N] = x . weight on E4M3: a dense projection with 128-deep scales.
 
-    x bf16 [T,H] is quantised per token and group of 128 (quantize_rows_group's rule).  ``weight`` is either bf16
+    x bf16 [T,H] is quantised per token and group of 128 (quantize_rows_block's rule).  ``weight`` is either bf16
     [H,N], quantised per block of 128 x 128 in the call (H and N multiples of 128): then the call is differentiable in
     both, dx from the E4M3 codes of dy (per token and 128 of N) and of the weight, dw = x^T dy as a bf16 product, the
     quantisation's own derivative taken as 1.  Or a pair (codes, descale) from quantize_block (serving; N a multiple

@@ -8,7 +8,7 @@ float32 rounding errors are measured on.
 
 import numpy as np
 
-from .quant import quantize_rows
+from .quant import round_e4m3
 
 GROUP = 128
 
@@ -68,16 +68,34 @@ def e4m3_values(codes):
     return np.where(c >> 7, -v, v)
 
 
+def _quantize(v):
+    """E4M3 values and float32 descales of rows v [n, L] (float32), one scale per row: 448 times the rounded reciprocal
+    of the largest, at most the largest float32; 1 for a row of zeros."""
+    v = np.asarray(v, np.float32)
+    m = np.max(np.abs(v), axis=-1)
+    with np.errstate(divide="ignore", over="ignore"):
+        s = np.minimum((np.float32(1.0) / m).astype(np.float32) * np.float32(448.0), np.finfo(np.float32).max)
+    s = np.where(m > 0, s, np.float32(1.0)).astype(np.float32)
+    q = round_e4m3((v * s[..., None]).astype(np.float32).astype(np.float64))
+    return q, (np.float32(1.0) / s).astype(np.float32)
+
+
+def quantize_rows_block(x):
+    """(E4M3 values [T,H], float32 descales [T,H/128]) of x [T,H]: one scale per token and group of 128."""
+    T, H = x.shape
+    q, d = _quantize(np.asarray(x, np.float32).reshape(T * (H // GROUP), GROUP))
+    return q.reshape(T, H), d.reshape(T, H // GROUP)
+
+
 def quantize_block(w):
-    """(E4M3 values [N,H], float32 descales [ceil(N/128), H/128]) of w [H,N]: one row of quantize_rows per block."""
+    """(E4M3 values [N,H], float32 descales [ceil(N/128), H/128]) of w [H,N], one scale per block."""
     H, N = w.shape
     nb, hb = (N + GROUP - 1) // GROUP, H // GROUP
     t = np.zeros((nb * GROUP, H), np.float32)
     t[:N] = np.asarray(w, np.float32).T
-    blocks = t.reshape(nb, GROUP, hb, GROUP).transpose(0, 2, 1, 3).reshape(nb * hb, GROUP * GROUP)
-    q, _, d = quantize_rows(blocks)
-    q = np.asarray(q, np.float64).reshape(nb, hb, GROUP, GROUP).transpose(0, 2, 1, 3).reshape(nb * GROUP, H)[:N]
-    return q, np.asarray(d, np.float32).reshape(nb, hb)
+    q, d = _quantize(t.reshape(nb, GROUP, hb, GROUP).transpose(0, 2, 1, 3).reshape(nb * hb, GROUP * GROUP))
+    q = q.reshape(nb, hb, GROUP, GROUP).transpose(0, 2, 1, 3).reshape(nb * GROUP, H)[:N]
+    return q, d.reshape(nb, hb)
 
 
 def block_product(xv, xs, wv, ws):

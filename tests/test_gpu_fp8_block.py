@@ -17,7 +17,6 @@ import torch
 
 from _util import announce, to_f64
 from oracle import block
-from oracle.quant import quantize_rows_groups
 
 pytestmark = pytest.mark.gpu
 CUT = 128 * 2.0 ** -13
@@ -48,8 +47,7 @@ def _check(y, xv, xs, wv, ws, what):
 
 
 def _tokens(x):
-    q, _, d = quantize_rows_groups(x.float().numpy())
-    return np.asarray(q, np.float64), np.asarray(d, np.float32)
+    return block.quantize_rows_block(x.float().numpy())
 
 
 @pytest.mark.parametrize("E,H,N", [(1, 128, 16), (1, 256, 144), (3, 384, 272), (2, 128, 128), (1, 1024, 1552)])
@@ -81,7 +79,9 @@ def test_few_rows(T, H, N):
     y = hmm.linear_fp8_block(x.cuda(), (codes, ds))
     xv, xs = _tokens(x)
     _check(y, xv, xs, block.e4m3_values(codes.cpu().numpy()), ds.cpu().numpy(), (T, H, N))
-    xq, xd = hmm.quantize_rows_group(x.cuda())
+    xq, xd = hmm.quantize_rows_block(x.cuda())
+    np.testing.assert_array_equal(block.e4m3_values(xq.cpu().numpy()), xv)
+    np.testing.assert_array_equal(xd.cpu().numpy(), xs)
     _check(hmm.matmul_fp8_block(xq, xd, codes, ds), xv, xs, block.e4m3_values(codes.cpu().numpy()), ds.cpu().numpy(), "codes")
 
 
@@ -97,7 +97,9 @@ def test_many_rows(T, H, N):
     y = hmm.linear_fp8_block(x.cuda(), (codes, ds))
     xv, xs = _tokens(x)
     _check(y, xv, xs, block.e4m3_values(codes.cpu().numpy()), ds.cpu().numpy(), (T, H, N))
-    xq, xd = hmm.quantize_rows_group(x.cuda())
+    xq, xd = hmm.quantize_rows_block(x.cuda())
+    np.testing.assert_array_equal(block.e4m3_values(xq.cpu().numpy()), xv)
+    np.testing.assert_array_equal(xd.cpu().numpy(), xs)
     assert torch.equal(hmm.matmul_fp8_block(xq, xd, codes, ds), y)
     # rows behind the last token stay as they were
     import ctypes
