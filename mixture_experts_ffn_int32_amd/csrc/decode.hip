@@ -33,13 +33,14 @@ namespace {
 
 constexpr int DT = DECODE_MAX_TOKENS;
 constexpr int MAX_SLOTS = DT * 16;
+constexpr int MAX_GROUPS = 512;   // workgroups of an expert launch: two a CU (all resident), each taking units in turn
 static_assert(DT == 64, "the rows of an expert are one 64-bit lane mask");
 
 // ------------------------------------------------------------------------ router
 
-// logits[t][e] in float64: a workgroup takes EE experts and TT tokens, its
+// logits[t][e] in float64: a workgroup takes GE experts and GT tokens, its
 // threads split H in 16-byte chunks.
-constexpr int GE = 2, GT = 4, GTHR = 512;
+constexpr int GTHR = 512;
 
 template <class W>
 __device__ __forceinline__ void router8(const W* p, double (&v)[8]);
@@ -61,7 +62,7 @@ __device__ __forceinline__ void router8<float>(const float* p, double (&v)[8]) {
   }
 }
 
-template <class W>
+template <class W, int GE, int GT>
 __global__ void __launch_bounds__(GTHR) router_logits(const uint16_t* __restrict__ x, const W* __restrict__ wr, int T,
                                                       int64_t H, int E, double* __restrict__ logits) {
   __shared__ double part[GTHR / 64][GE * GT];
@@ -98,120 +99,115 @@ __global__ void __launch_bounds__(GTHR) router_logits(const uint16_t* __restrict
   }
 }
 
-// One wave per token: K times the largest remaining logit (ties to the lower
-// index, a NaN ranks last), then the weights: exp(l - max) over its sum over the
-// chosen (renorm) or over all experts.
-constexpr int TK_PER = MAX_EXPERTS / 64;
-__global__ void __launch_bounds__(64) router_topk(const double* __restrict__ logits, int E, int K, int renorm,
+// One workgroup per token, one thread per expert: an expert's rank is the number of
+// experts before it (a larger logit, or the same and a lower index; a NaN counts as
+// -infinity), and ranks below K are the choice.  Then the weights: exp(l - max) over its
+// sum over the chosen (renorm) or over all experts, added in a fixed order.
+template <int NT>
+__global__ void __launch_bounds__(NT) router_topk(const double* __restrict__ logits, int E, int K, int renorm,
                                                   int32_t* __restrict__ ids, float* __restrict__ weights) {
-  const int t = blockIdx.x, lane = threadIdx.x;
-  double v[TK_PER];
-  uint32_t open = 0;  // bit j: expert lane + 64 j is still to be chosen
-#pragma unroll
-  for (int j = 0; j < TK_PER; ++j) {
-    v[j] = -__builtin_inf();
-    if (64 * j < E && lane + 64 * j < E) {
-      const double l = logits[(int64_t)t * E + lane + 64 * j];
-      if (l == l) v[j] = l;
-      open |= 1u << j;
-    }
+  __shared__ __attribute__((aligned(16))) double l[NT + 2];
+  __shared__ float chosen[16];
+  __shared__ float part[NT / 64];
+  __shared__ double top;
+  const int t = blockIdx.x, e = threadIdx.x;
+  double v = -__builtin_inf();
+  if (e < E) {
+    const double x = logits[(int64_t)t * E + e];
+    if (x == x) v = x;
   }
-  double top = 0.;
-  float mine = 0.f, sum = 0.f;
-  int my_id = 0;
-  for (int k = 0; k < K; ++k) {
-    double b = -__builtin_inf();
-    int bi = 0x7fffffff;
-#pragma unroll
-    for (int j = 0; j < TK_PER; ++j)
-      if (64 * j < E && ((open >> j) & 1) && (bi == 0x7fffffff || v[j] > b)) {
-        b = v[j];
-        bi = lane + 64 * j;
-      }
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) {
-      const double ob = __shfl_xor(b, d);
-      const int oi = __shfl_xor(bi, d);
-      if (oi != 0x7fffffff && (bi == 0x7fffffff || ob > b || (ob == b && oi < bi))) {
-        b = ob;
-        bi = oi;
-      }
+  l[e] = v;
+  __syncthreads();
+  int rank = 0;
+  if (e < E) {
+    const double2* p = reinterpret_cast<const double2*>(l);
+    // threads past E hold -infinity at a higher index: they are before nobody
+#pragma unroll 4
+    for (int j = 0; j < E; j += 2) {
+      const double2 o = p[j >> 1];
+      rank += (o.x > v) | ((o.x == v) & (j < e));
+      rank += (o.y > v) | ((o.y == v) & (j + 1 < e));
     }
-    if (k == 0) top = b;
-    const float e = expf((float)(b - top));
-    sum += e;
-    if (lane == k) {
-      mine = e;
-      my_id = bi;
-    }
-    if ((bi & 63) == lane) open &= ~(1u << (bi >> 6));
+    if (rank == 0) top = v;
+  }
+  __syncthreads();
+  const float x = e < E ? expf((float)(v - top)) : 0.f;
+  if (e < E && rank < K) {
+    ids[t * K + rank] = e;
+    chosen[rank] = x;
   }
   if (!renorm) {
-    sum = 0.f;
+    float s = x;
 #pragma unroll
-    for (int j = 0; j < TK_PER; ++j)
-      if (64 * j < E && lane + 64 * j < E) sum += expf((float)(v[j] - top));
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) sum += __shfl_xor(sum, d);
+    for (int d = 32; d >= 1; d >>= 1) s += __shfl_xor(s, d);
+    if ((e & 63) == 0) part[e >> 6] = s;
   }
-  if (lane < K) {
-    ids[t * K + lane] = my_id;
-    weights[t * K + lane] = mine / sum;
+  __syncthreads();
+  if (e < K) {
+    float sum = 0.f;
+    if (renorm)
+      for (int k = 0; k < K; ++k) sum += chosen[k];
+    else
+      for (int k = 0; k < NT / 64; ++k) sum += part[k];
+    weights[t * K + e] = chosen[e] / sum;
   }
 }
 
 // ------------------------------------------------------------------- expert tiles
 
-// What a workgroup finds out first: the i-th expert that some token chose, and
-// the rows (tokens) it has.  A token that names an expert twice is one row.
-struct Rows {
+// What a workgroup finds out first: the experts that some token chose, in ascending order.
+struct Chosen {
   int32_t ids[MAX_SLOTS];
-  uint32_t chosen[MAX_EXPERTS / 32];
-  int32_t tok[DT];
-  int32_t slot[DT];  // t * K + the first k that names the expert
+  uint32_t bits[MAX_EXPERTS / 32];
+  uint16_t expert[MAX_EXPERTS];
   int flag;
 };
 
-// false if fewer than i + 1 experts are chosen; nact: how many are
+// LDS written before is readable after, by every wave; loads from global memory stay in flight
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// returns how many experts are chosen
 template <int DW>
-__device__ __forceinline__ bool find_rows(Rows& L, const DecodeArgs& A, int i, int& e, int& rows, int& nact) {
-  const int tid = threadIdx.x, lane = tid & 63;
+__device__ __forceinline__ int find_chosen(Chosen& L, const DecodeArgs& A) {
+  const int tid = threadIdx.x;
   const int S = A.T * A.K;
-  if (tid < MAX_EXPERTS / 32) L.chosen[tid] = 0;
+  if (tid < MAX_EXPERTS / 32) L.bits[tid] = 0;
   __syncthreads();
   for (int s = tid; s < S; s += DW * 64) {
     const int id = A.ids[s];
     L.ids[s] = id;
-    if (id >= 0 && id < A.E) atomicOr(&L.chosen[id >> 5], 1u << (id & 31));
+    if (id >= 0 && id < A.E) atomicOr(&L.bits[id >> 5], 1u << (id & 31));
   }
   __syncthreads();
-  const uint32_t w = lane < MAX_EXPERTS / 32 ? L.chosen[lane] : 0u;
+  const int lane = tid & 63;
+  uint32_t w = lane < MAX_EXPERTS / 32 ? L.bits[lane] : 0u;
   int inc = __popc(w);
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
     const int o = __shfl_up(inc, d);
     if (lane >= d) inc += o;
   }
-  nact = __shfl(inc, 31);
-  if (i >= nact) return false;
-  const int word = __ffsll((unsigned long long)__ballot(lane < 32 && inc > i)) - 1;
-  uint32_t bits = (uint32_t)__shfl((int)w, word);
-  int skip = i - (__shfl(inc, word) - __popc(bits));
-  while (skip--) bits &= bits - 1;
-  e = word * 32 + __ffs(bits) - 1;
+  if (tid < MAX_EXPERTS / 32)
+    for (int at = inc - __popc(w); w; w &= w - 1) L.expert[at++] = (uint16_t)(tid * 32 + __ffs(w) - 1);
+  __syncthreads();
+  return __builtin_amdgcn_readfirstlane(__shfl(inc, 31));
+}
+
+// The rows (tokens) of an expert, found by a wave on its own: their number, and in
+// lane r the slot t K + k of row r (k: the first that names the expert; a token that
+// names it twice is one row).
+__device__ __forceinline__ int find_rows(const Chosen& L, const DecodeArgs& A, int e, int lane, int& slot) {
   int first = -1;
   if (lane < A.T)
     for (int k = A.K - 1; k >= 0; --k)
       if (L.ids[lane * A.K + k] == e) first = k;
   const uint64_t mask = __ballot(first >= 0);
-  rows = __popcll(mask);
-  if (first >= 0 && tid < 64) {
-    const int r = __popcll(mask & ((1ull << lane) - 1));
-    L.tok[r] = lane;
-    L.slot[r] = lane * A.K + first;
-  }
-  __syncthreads();
-  return true;
+  const int rows = __popcll(mask);
+  const uint64_t below = mask & ((1ull << lane) - 1);
+  // rows go to the lowest lanes in order, the other lanes behind them: a permutation
+  const int to = first >= 0 ? __popcll(below) : rows + lane - __popcll(below);
+  slot = __builtin_amdgcn_ds_permute(4 * to, lane * A.K + first);
+  return rows;
 }
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
@@ -255,7 +251,7 @@ struct Bf16Weights {
         a[q] = __builtin_amdgcn_perm(r[2 * q + 1][c >> 1], r[2 * q][c >> 1], (c & 1) ? 0x07060302u : 0x05040100u);
 #pragma unroll
       for (int n = 0; n < NT; ++n)
-        if (n < nt)
+        if (NT == 1 || n < nt)
 #pragma unroll
           for (int h = 0; h < PARTS; ++h)
             acc[c][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
@@ -314,7 +310,7 @@ struct Fp8Weights {
       const float s = c < 2 ? s0 : s1;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
-        if (n < nt) {
+        if (NT == 1 || n < nt) {
           f32x4 g = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int q = 0; q < 2 * CL; ++q)
@@ -329,51 +325,99 @@ struct Fp8Weights {
   }
 };
 
-// The wave's sums over its steps (wave, wave + DW, ...) of the tile.  src[n]: this
-// lane's row of row tile n (rows past the last one repeat row 0's data: their
-// columns of the accumulator are never read); part: elements between a row's parts.
-template <class WT, int NT, int PARTS, int DW>
-__device__ __forceinline__ void stream_tile(const WT& W, const uint16_t* const (&src)[NT], int64_t part, int steps,
-                                            int wave, int lane, int nt, f32x4 (&acc)[WT::SUB][NT]) {
-#pragma unroll
-  for (int c = 0; c < WT::SUB; ++c)
-#pragma unroll
-    for (int n = 0; n < NT; ++n) acc[c][n] = f32x4{0.f, 0.f, 0.f, 0.f};
-  if (wave >= steps) return;
-  // The loads return in order: with one row tile its data is fetched a step ahead
-  // with the weights; with more (registers) right before the next step's weights, so
-  // that waiting for it leaves those in flight.
-  constexpr bool AHEAD = NT == 1;
-  u32x4 w[WT::LOADS], b[NT][PARTS][WT::ROW_LOADS];
-  auto load_rows = [&](int s, u32x4 (&br)[NT][PARTS][WT::ROW_LOADS]) {
+// A unit of work: a column tile of one expert, for up to 16 NT of its rows (an expert with
+// more takes the tile again for the next ones).
+template <class WT, int NT>
+struct Unit {
+  int index, chunk;           // unit number, chunk of 16 NT rows
+  int e, tile, rows, nt;      // rows of the expert; row tiles of this chunk
+  int slot;                   // lane r: slot of the expert's row r
+  WT W;
+  const uint16_t* src[NT];    // this lane's row of each row tile
+};
+
+// The waves of a tile take the steps of a unit in turn: first, first + DS, ... and load one
+// step ahead, across the end of a unit into the next one.  ``next()`` fills a unit with the
+// following one and is false at the end.  The rows of a step are fetched with its weights
+// (NT == 1), or right before the next step's weights, so that waiting for them leaves those
+// in flight (loads return in order).  Rows past the last one repeat row 0: their columns of
+// the accumulator are never read.
+template <class WT, int NT, int PARTS, int DS>
+struct Stream {
+  static constexpr bool AHEAD = NT == 1;
+  u32x4 w[2][WT::LOADS], b[AHEAD ? 2 : 1][NT][PARTS][WT::ROW_LOADS];
+  f32x4 acc[WT::SUB][NT];
+
+  template <int P>
+  __device__ __forceinline__ void load_rows(const Unit<WT, NT>& U, int s, int64_t part) {
 #pragma unroll
     for (int n = 0; n < NT; ++n)
-      if (n < nt)
+      if (NT == 1 || n < U.nt)
 #pragma unroll
         for (int h = 0; h < PARTS; ++h)
 #pragma unroll
           for (int q = 0; q < WT::ROW_LOADS; ++q)
-            br[n][h][q] = *reinterpret_cast<const u32x4*>(src[n] + h * part + (int64_t)s * WT::DEPTH + 8 * q);
-  };
-  W.load(wave, w);
-  if constexpr (AHEAD) load_rows(wave, b);
-  for (int s = wave; s < steps; s += DW) {
-    u32x4 wn[WT::LOADS], bn[NT][PARTS][WT::ROW_LOADS];
-    if constexpr (!AHEAD) load_rows(s, b);
-    if (s + DW < steps) {
-      W.load(s + DW, wn);
-      if constexpr (AHEAD) load_rows(s + DW, bn);
-    }
-    W.template mul<NT, PARTS>(s, w, b, nt, acc);
-#pragma unroll
-    for (int j = 0; j < WT::LOADS; ++j) w[j] = wn[j];
-    if constexpr (AHEAD)
-#pragma unroll
-      for (int h = 0; h < PARTS; ++h)
-#pragma unroll
-        for (int q = 0; q < WT::ROW_LOADS; ++q) b[0][h][q] = bn[0][h][q];
+            b[AHEAD ? P : 0][n][h][q] = *reinterpret_cast<const u32x4*>(U.src[n] + h * part + (int64_t)s * WT::DEPTH + 8 * q);
   }
-}
+  // step s into register set P
+  template <int P>
+  __device__ __forceinline__ void load(const Unit<WT, NT>& U, int s, int64_t part) {
+    U.W.load(s, w[P]);
+    if constexpr (AHEAD) load_rows<P>(U, s, part);
+    __builtin_amdgcn_sched_barrier(0);  // the loads go out here, not where their data is needed
+  }
+  // step s from register set P; the rows now, where they are not fetched ahead
+  template <int P>
+  __device__ __forceinline__ void rows_now(const Unit<WT, NT>& U, int s, int64_t part) {
+    if constexpr (!AHEAD) load_rows<0>(U, s, part);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  template <int P>
+  __device__ __forceinline__ void mul(const Unit<WT, NT>& U, int s) {
+    U.W.template mul<NT, PARTS>(s, w[P], b[AHEAD ? P : 0], U.nt, acc);
+  }
+  __device__ __forceinline__ void begin(const Unit<WT, NT>& U, int64_t part, int steps, int first) {
+    if (first < steps) load<0>(U, first, part);
+  }
+  // The sums of U's steps; then U is the next unit with its first step on the way in set 0,
+  // or the result is false.
+  template <class Next>
+  __device__ __forceinline__ bool run(Unit<WT, NT>& U, int64_t part, int steps, int first, Next&& next) {
+#pragma unroll
+    for (int c = 0; c < WT::SUB; ++c)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) acc[c][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+    int s = first;
+    for (; s + 2 * DS < steps; s += 2 * DS) {
+      rows_now<0>(U, s, part);
+      load<1>(U, s + DS, part);
+      mul<0>(U, s);
+      rows_now<1>(U, s + DS, part);
+      load<0>(U, s + 2 * DS, part);
+      mul<1>(U, s + DS);
+    }
+    if (s + DS < steps) {
+      rows_now<0>(U, s, part);
+      load<1>(U, s + DS, part);
+      mul<0>(U, s);
+      s += DS;
+      rows_now<1>(U, s, part);
+      Unit<WT, NT> V = U;
+      const bool more = next(V);
+      if (more) load<0>(V, first, part);
+      mul<1>(U, s);
+      U = V;
+      return more;
+    }
+    if (s < steps) {
+      rows_now<0>(U, s, part);
+      mul<0>(U, s);
+    }
+    const bool more = next(U);
+    if (more && first < steps) load<0>(U, first, part);
+    return more;
+  }
+};
 
 // LDS of the waves' sums of one row tile: [DW][16 rows][COLS + 4] floats (a pitch of
 // 4 banks more than a multiple of 64: the 16 rows of a store fall into distinct banks)
@@ -389,153 +433,292 @@ __device__ __forceinline__ void put_sums(Sums<WT, DW>& L, const f32x4 (&acc)[WT:
 #pragma unroll
     for (int i = 0; i < 4; ++i) L.v[wave][lane & 15][WT::column(c, 4 * (lane >> 4) + i)] = acc[c][n][i];
 }
-template <class WT, int DW>
-__device__ __forceinline__ float get_sum(const Sums<WT, DW>& L, int row, int col) {
+// the sum of the waves [first, first + N)
+template <int N, class WT, int DW>
+__device__ __forceinline__ float get_sum(const Sums<WT, DW>& L, int first, int row, int col) {
   float s = 0.f;
 #pragma unroll
-  for (int q = 0; q < DW; ++q) s += L.v[q][row][col];
+  for (int q = 0; q < N; ++q) s += L.v[first + q][row][col];
   return s;
 }
 
-// up-projection: COLS / 2 gate columns and the matching up columns of one expert
-template <class WT, int NT, int DW>
-__global__ void __launch_bounds__(DW * 64) decode_up(const DecodeArgs A) {
-  constexpr int HC = WT::COLS / 2;
-  __shared__ Rows L;
+// up-projection: HC gate columns and the matching up columns of one expert a unit.  Narrow:
+// every wave has COLS / 2 of each.  Wide: half of the waves have COLS gate columns, the
+// others the up columns, so that a row's bytes lie together (bf16: 256 instead of twice 128).
+template <class WT, int NT, int DW, bool WIDE>
+__global__ void __launch_bounds__(DW * 64, 2) decode_up(const DecodeArgs A) {
+  constexpr int HC = WIDE ? WT::COLS : WT::COLS / 2, DS = WIDE ? DW / 2 : DW;
+  __shared__ Chosen L;
   __shared__ Sums<WT, DW> P;
-  const int tiles = (int)(A.I / HC);
+  const int tiles = (int)(A.I / HC), steps = (int)(A.H / WT::DEPTH);
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   // the down-projection's counters, cleared one launch ahead of their use
   for (int64_t g = (int64_t)blockIdx.x * DW * 64 + threadIdx.x; g < A.col_tiles; g += (int64_t)gridDim.x * DW * 64)
     A.count[g] = 0;
-  int e, rows, nact;
-  const int n0 = (blockIdx.x % tiles) * HC;
-  if (!find_rows<DW>(L, A, blockIdx.x / tiles, e, rows, nact)) return;
-  e = __builtin_amdgcn_readfirstlane(e);
-  const int nt = __builtin_amdgcn_readfirstlane((rows + 15) >> 4);
-  WT W;
-  W.init(static_cast<const char*>(A.up) + (int64_t)e * A.H * 2 * A.I * A.wbytes, A.H, 2 * A.I, n0, A.I + n0,
-         A.up_descale + (int64_t)e * (2 * A.I / 128) * (A.H / 128), A.H / 128, lane);
-  const uint16_t* src[NT];
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const int r = n * 16 + (lane & 15);
-    src[n] = A.x + (int64_t)L.tok[r < rows ? r : 0] * A.H + WT::row_offset(lane);
-  }
-  f32x4 acc[WT::SUB][NT];
-  stream_tile<WT, NT, 1, DW>(W, src, 0, (int)(A.H / WT::DEPTH), wave, lane, nt, acc);
-  for (int n = 0; n < nt; ++n) {
-#pragma unroll
-    for (int q = 0; q < NT; ++q)
-      if (q == n) put_sums<WT, NT, DW>(P, acc, q, wave, lane);
-    __syncthreads();
-    for (int i = threadIdx.x; i < 16 * HC; i += DW * 64) {
-      const int row = n * 16 + i / HC, col = i % HC;
-      if (row < rows) {
-        const float gv = get_sum(P, i / HC, col), u = get_sum(P, i / HC, HC + col);
-        const float a = gv * sigmoidf_(gv) * u;
-        uint16_t* out = A.a + (int64_t)L.slot[row] * 2 * A.I + n0 + col;
-        const uint16_t hi = f2bf(a);
-        const float rest = a - bf2f(hi);
-        out[0] = hi;
-        out[A.I] = __builtin_isfinite(rest) ? f2bf(rest) : 0;  // an infinite a has no rest
-      }
-    }
-    __syncthreads();
-  }
-}
-
-// down-projection: COLS columns of one expert's rows, then, by the workgroup that
-// finishes the column tile, the weighted sum of each token's rows
-template <class WT, int NT, int DW>
-__global__ void __launch_bounds__(DW * 64) decode_down(const DecodeArgs A) {
-  constexpr int C = WT::COLS;
-  __shared__ Rows L;
-  __shared__ Sums<WT, DW> P;
-  const int tiles = A.col_tiles;
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-  const int ct = blockIdx.x % tiles;
-  const int n0 = ct * C;
-  const int width = min(C, (int)A.H - n0);  // H is a multiple of 64: a last tile may be half as wide
-  int e, rows, nact;
-  const int i = blockIdx.x / tiles;
-  const bool have = find_rows<DW>(L, A, i, e, rows, nact);
-  if (!have && !(i == 0 && nact == 0)) return;
-  const rsrc_t o = make_rsrc(A.o, (int64_t)A.T * A.K * A.H * 4);
-  bool last = true;
-  if (have) {
-    e = __builtin_amdgcn_readfirstlane(e);
-    const int nt = __builtin_amdgcn_readfirstlane((rows + 15) >> 4);
-    // a half tile's missing columns read its first half again (and are not stored)
-    const int64_t c1 = width > C / 2 ? n0 + C / 2 : n0;
-    WT W;
-    W.init(static_cast<const char*>(A.down) + (int64_t)e * A.H * A.I * A.wbytes, A.I, A.H, n0, c1,
-           A.down_descale + (int64_t)e * (A.H / 128) * (A.I / 128), A.I / 128, lane);
-    const uint16_t* src[NT];
+  const int units = find_chosen<DW>(L, A) * tiles;
+  typedef Unit<WT, NT> U;
+  auto rows_of = [&](U& u) {
+    u.nt = min(NT, (u.rows - u.chunk * 16 * NT + 15) >> 4);
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const int r = n * 16 + (lane & 15);
-      src[n] = A.a + (int64_t)L.slot[r < rows ? r : 0] * 2 * A.I + WT::row_offset(lane);
+      const int r = (u.chunk * NT + n) * 16 + (lane & 15);
+      const int slot = __shfl(u.slot, r < u.rows ? r : 0);
+      u.src[n] = A.x + (int64_t)(slot / A.K) * A.H + WT::row_offset(lane);
     }
-    f32x4 acc[WT::SUB][NT];
-    stream_tile<WT, NT, 2, DW>(W, src, A.I, (int)(A.I / WT::DEPTH), wave, lane, nt, acc);
+  };
+  auto set = [&](U& u, int index) {
+    u.index = index;
+    u.chunk = 0;
+    u.tile = index % tiles;
+    u.e = __builtin_amdgcn_readfirstlane((int)L.expert[index / tiles]);
+    u.rows = __builtin_amdgcn_readfirstlane(find_rows(L, A, u.e, lane, u.slot));
+    const int64_t n0 = (int64_t)u.tile * HC;
+    u.W.init(static_cast<const char*>(A.up) + (int64_t)u.e * A.H * 2 * A.I * A.wbytes, A.H, 2 * A.I,
+             WIDE && wave >= DS ? A.I + n0 : n0, WIDE ? (wave >= DS ? A.I : 0) + n0 + HC / 2 : A.I + n0,
+             A.up_descale + (int64_t)u.e * (2 * A.I / 128) * (A.H / 128), A.H / 128, lane);
+    rows_of(u);
+  };
+  auto next = [&](U& u) {
+    if ((u.chunk + 1) * 16 * NT < u.rows) {
+      ++u.chunk;
+      rows_of(u);
+      return true;
+    }
+    const int index = u.index + (int)gridDim.x;
+    if (index >= units) return false;
+    set(u, index);
+    return true;
+  };
+  if ((int)blockIdx.x >= units) return;
+  U u;
+  set(u, blockIdx.x);
+  Stream<WT, NT, 1, DS> S;
+  const int first = WIDE && wave >= DS ? wave - DS : wave;
+  S.begin(u, 0, steps, first);
+  for (bool more = true; more;) {
+    const int nt = u.nt, row0 = u.chunk * 16 * NT, rows = u.rows, n0 = u.tile * HC, slot_of = u.slot;
+    more = S.run(u, 0, steps, first, next);
     for (int n = 0; n < nt; ++n) {
 #pragma unroll
       for (int q = 0; q < NT; ++q)
-        if (q == n) put_sums<WT, NT, DW>(P, acc, q, wave, lane);
-      __syncthreads();
-      for (int c = threadIdx.x; c < 16 * C / 4; c += DW * 64) {
-        const int row = n * 16 + c / (C / 4), col = c % (C / 4) * 4;
-        if (row < rows && col < width) {
-          f32x4 v;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) v[j] = get_sum(P, c / (C / 4), col + j);
-          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), o,
-                                                 (int)(uint32_t)(((int64_t)L.slot[row] * A.H + n0 + col) * 4), 0, 16);
+        if (q == n) put_sums<WT, NT, DW>(P, S.acc, q, wave, lane);
+      lds_barrier();
+      for (int i = threadIdx.x; i < 16 * HC; i += DW * 64) {
+        const int row = row0 + n * 16 + i / HC, col = i % HC;
+        const int slot = __shfl(slot_of, row & 63);
+        if (row < rows) {
+          const float gv = get_sum<DS>(P, 0, i / HC, col);
+          const float uv = get_sum<DS>(P, DW - DS, i / HC, WIDE ? col : HC + col);
+          const float a = gv * sigmoidf_(gv) * uv;
+          uint16_t* out = A.a + (int64_t)slot * 2 * A.I + n0 + col;
+          const uint16_t hi = f2bf(a);
+          const float rest = a - bf2f(hi);
+          out[0] = hi;
+          out[A.I] = __builtin_isfinite(rest) ? f2bf(rest) : 0;  // an infinite a has no rest
         }
       }
-      __syncthreads();
+      lds_barrier();
     }
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the rows have reached the coherence point
-    __syncthreads();
-    if (threadIdx.x == 0)
-      L.flag = __hip_atomic_fetch_add(A.count + ct, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)nact - 1;
-    __syncthreads();
-    last = L.flag != 0;
-  }
-  if (!last) return;
-  const int cpr = width / 4;
-  for (int c = threadIdx.x; c < A.T * cpr; c += DW * 64) {
-    const int t = c / cpr, col = n0 + c % cpr * 4;
-    f32x4 y = {0.f, 0.f, 0.f, 0.f};
-    for (int k = 0; k < A.K; ++k) {
-      const int id = L.ids[t * A.K + k];
-      if (id < 0 || id >= A.E) continue;
-      int first = k;
-      for (int q = 0; q < k; ++q)
-        if (L.ids[t * A.K + q] == id) {
-          first = q;
-          break;
-        }
-      const float w = A.weights[t * A.K + k];
-      const f32x4 v = __builtin_bit_cast(f32x4, bload_coh(o, (uint32_t)(((int64_t)(t * A.K + first) * A.H + col) * 4), 0));
-#pragma unroll
-      for (int j = 0; j < 4; ++j) y[j] = __builtin_fmaf(w, v[j], y[j]);
-    }
-    uint2 out;
-    out.x = (uint32_t)f2bf(y[0]) | ((uint32_t)f2bf(y[1]) << 16);
-    out.y = (uint32_t)f2bf(y[2]) | ((uint32_t)f2bf(y[3]) << 16);
-    *reinterpret_cast<uint2*>(A.y + (int64_t)t * A.H + col) = out;
   }
 }
 
-template <class WT, int NT, int DW>
+// The weighted sum of a token's rows at 4 columns, in the order of its slots, four rows'
+// loads at a time.  COH: the rows were written in this launch.
+template <bool COH, class Ids>
+__device__ __forceinline__ void combine4(const Ids& ids, const DecodeArgs& A, rsrc_t o, int t, int col) {
+  f32x4 y = {0.f, 0.f, 0.f, 0.f};
+  for (int k0 = 0; k0 < A.K; k0 += 4) {
+    f32x4 v[4];
+    float w[4];
+    bool has[4];  // a dropped slot adds nothing, whatever its weight
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int k = k0 + j;
+      w[j] = 0.f;
+      has[j] = false;
+      v[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if (k >= A.K) continue;
+      const int id = ids[t * A.K + k];
+      if (id < 0 || id >= A.E) continue;
+      int first = 0;  // a repeated expert's row is that of its first slot
+      while (ids[t * A.K + first] != id) ++first;
+      has[j] = true;
+      w[j] = A.weights[t * A.K + k];
+      const uint32_t at = (uint32_t)(((int64_t)(t * A.K + first) * A.H + col) * 4);
+      v[j] = __builtin_bit_cast(f32x4, COH ? bload_coh(o, at, 0) : bload(o, at, 0));
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (has[j])
+#pragma unroll
+        for (int q = 0; q < 4; ++q) y[q] = __builtin_fmaf(w[j], v[j][q], y[q]);
+  }
+  uint2 out;
+  out.x = (uint32_t)f2bf(y[0]) | ((uint32_t)f2bf(y[1]) << 16);
+  out.y = (uint32_t)f2bf(y[2]) | ((uint32_t)f2bf(y[3]) << 16);
+  *reinterpret_cast<uint2*>(A.y + (int64_t)t * A.H + col) = out;
+}
+
+template <int THREADS>
+__device__ __forceinline__ void combine_tile(const Chosen& L, const DecodeArgs& A, rsrc_t o, int n0, int width) {
+  const int cpr = width / 4;
+  for (int c = threadIdx.x; c < A.T * cpr; c += THREADS) combine4<true>(L.ids, A, o, c / cpr, n0 + c % cpr * 4);
+}
+
+constexpr int CT = 256;
+__global__ void __launch_bounds__(CT) decode_combine(const DecodeArgs A) {
+  const rsrc_t o = make_rsrc(A.o, (int64_t)A.T * A.K * A.H * 4);
+  const int col = (blockIdx.x * CT + threadIdx.x) * 4;
+  if (col < A.H) combine4<false>(A.ids, A, o, blockIdx.y, col);
+}
+
+// down-projection: CS COLS columns of one expert's rows a unit (a CS-th of the waves for each
+// COLS of them), then (SUM) by the workgroup that finishes the column tile the weighted sum of
+// each token's rows
+template <class WT, int NT, int DW, int CS, bool SUM>
+__global__ void __launch_bounds__(DW * 64, 2) decode_down(const DecodeArgs A) {
+  constexpr int C = WT::COLS * CS, DS = DW / CS;
+  __shared__ Chosen L;
+  __shared__ Sums<WT, DW> P;
+  const int tiles = (int)((A.H + C - 1) / C), steps = (int)(A.I / WT::DEPTH);
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int nact = find_chosen<DW>(L, A), units = nact * tiles;
+  const rsrc_t o = make_rsrc(A.o, (int64_t)A.T * A.K * A.H * 4);
+  // H is a multiple of 64: a last tile may be narrower
+  auto width_of = [&](int tile) { return min(C, (int)A.H - tile * C); };
+  if (SUM && units == 0)  // no valid id at all: y is zero
+    for (int t = blockIdx.x; t < tiles; t += gridDim.x) combine_tile<DW * 64>(L, A, o, t * C, width_of(t));
+  typedef Unit<WT, NT> U;
+  auto rows_of = [&](U& u) {
+    u.nt = min(NT, (u.rows - u.chunk * 16 * NT + 15) >> 4);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int r = (u.chunk * NT + n) * 16 + (lane & 15);
+      u.src[n] = A.a + (int64_t)__shfl(u.slot, r < u.rows ? r : 0) * 2 * A.I + WT::row_offset(lane);
+    }
+  };
+  auto set = [&](U& u, int index) {
+    u.index = index;
+    u.chunk = 0;
+    u.tile = index % tiles;
+    u.e = __builtin_amdgcn_readfirstlane((int)L.expert[index / tiles]);
+    u.rows = __builtin_amdgcn_readfirstlane(find_rows(L, A, u.e, lane, u.slot));
+    // columns past the last one: the wave reads its first half, or the tile, again (and does not store it)
+    int64_t n0 = (int64_t)u.tile * C + wave / DS * WT::COLS;
+    if (n0 >= A.H) n0 = (int64_t)u.tile * C;
+    u.W.init(static_cast<const char*>(A.down) + (int64_t)u.e * A.H * A.I * A.wbytes, A.I, A.H, n0,
+             n0 + WT::COLS / 2 < A.H ? n0 + WT::COLS / 2 : n0, A.down_descale + (int64_t)u.e * (A.H / 128) * (A.I / 128), A.I / 128,
+             lane);
+    rows_of(u);
+  };
+  auto next = [&](U& u) {
+    if ((u.chunk + 1) * 16 * NT < u.rows) {
+      ++u.chunk;
+      rows_of(u);
+      return true;
+    }
+    const int index = u.index + (int)gridDim.x;
+    if (index >= units) return false;
+    set(u, index);
+    return true;
+  };
+  if ((int)blockIdx.x >= units) return;
+  U u;
+  set(u, blockIdx.x);
+  Stream<WT, NT, 2, DS> S;
+  const int first = wave % DS;
+  S.begin(u, A.I, steps, first);
+  for (bool more = true; more;) {
+    const int nt = u.nt, row0 = u.chunk * 16 * NT, rows = u.rows, tile = u.tile, slot_of = u.slot;
+    const int n0 = tile * C, width = width_of(tile);
+    const bool done = row0 + 16 * NT >= rows;  // the expert's last chunk
+    more = S.run(u, A.I, steps, first, next);
+    for (int n = 0; n < nt; ++n) {
+#pragma unroll
+      for (int q = 0; q < NT; ++q)
+        if (q == n) put_sums<WT, NT, DW>(P, S.acc, q, wave, lane);
+      lds_barrier();
+      for (int c = threadIdx.x; c < 16 * C / 4; c += DW * 64) {
+        const int row = row0 + n * 16 + c / (C / 4), col = c % (C / 4) * 4;
+        const int slot = __shfl(slot_of, row & 63);
+        if (row < rows && col < width) {
+          f32x4 v;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[j] = get_sum<DS>(P, col / WT::COLS * DS, c / (C / 4), col % WT::COLS + j);
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), o,
+                                                 (int)(uint32_t)(((int64_t)slot * A.H + n0 + col) * 4), 0, SUM ? 16 : 0);
+        }
+      }
+      lds_barrier();
+    }
+    if (!SUM || !done) continue;
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the rows have reached the coherence point
+    lds_barrier();
+    if (threadIdx.x == 0)
+      L.flag = __hip_atomic_fetch_add(A.count + tile, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)nact - 1;
+    __syncthreads();
+    if (L.flag) combine_tile<DW * 64>(L, A, o, n0, width);
+    lds_barrier();  // the flag has been read
+  }
+}
+
+// one token: a workgroup per expert (four tokens would only repeat it)
+template <class W>
+void launch_logits(const uint16_t* x, const W* wr, int T, int64_t H, int E, double* logits, hipStream_t stream) {
+  if (T == 1)
+    router_logits<W, 1, 1><<<E, GTHR, 0, stream>>>(x, wr, T, H, E, logits);
+  else
+    router_logits<W, 2, 4><<<dim3((E + 1) / 2, (T + 3) / 4), GTHR, 0, stream>>>(x, wr, T, H, E, logits);
+}
+
+template <class WT, int NT, int DW, bool WIDE>
+void launch_up(const DecodeArgs& A, int64_t act, hipStream_t stream) {
+  const int64_t units = act * (A.I / (WIDE ? WT::COLS : WT::COLS / 2));
+  decode_up<WT, NT, DW, WIDE><<<(unsigned)(units < MAX_GROUPS ? units : MAX_GROUPS), DW * 64, 0, stream>>>(A);
+}
+template <class WT, int NT, int DW, int CS, bool SUM>
+void launch_down(const DecodeArgs& A, int64_t act, hipStream_t stream) {
+  const int64_t units = act * ((A.H + WT::COLS * CS - 1) / (WT::COLS * CS));
+  decode_down<WT, NT, DW, CS, SUM><<<(unsigned)(units < MAX_GROUPS ? units : MAX_GROUPS), DW * 64, 0, stream>>>(A);
+}
+
+constexpr int SUM_TOKENS = 4;
+
+// WA: weights of up to 16 tokens (one row tile), WB: of more
+template <class WA, class WB, int DW>
 hipError_t launch_experts(const DecodeArgs& A, hipStream_t stream) {
-  const int64_t act = A.E < A.T * A.K ? A.E : A.T * A.K;
-  decode_up<WT, NT, DW><<<(unsigned)(act * (A.I / (WT::COLS / 2))), DW * 64, 0, stream>>>(A);
-  decode_down<WT, NT, DW><<<(unsigned)(act * A.col_tiles), DW * 64, 0, stream>>>(A);
+  const int64_t act = A.E < A.T * A.K ? A.E : A.T * A.K;  // experts that may be chosen
+  const bool wide = A.wbytes == 2 && A.I % 128 == 0 && act * (A.I / 128) >= MAX_GROUPS;
+  if (A.T <= 16) {
+    if (wide)
+      launch_up<WA, 1, DW, true>(A, act, stream);
+    else
+      launch_up<WA, 1, DW, false>(A, act, stream);
+  } else {
+    if (wide)
+      launch_up<WB, 2, DW, true>(A, act, stream);
+    else
+      launch_up<WB, 2, DW, false>(A, act, stream);
+  }
+  if (A.T <= SUM_TOKENS) {
+    launch_down<WA, 1, DW, 1, true>(A, act, stream);
+    return hipGetLastError();
+  }
+  const bool wider = A.wbytes == 2 && act * (A.H / (2 * WA::COLS)) >= MAX_GROUPS;
+  if (A.T <= 16) {
+    if (wider)
+      launch_down<WA, 1, DW, 2, false>(A, act, stream);
+    else
+      launch_down<WA, 1, DW, 1, false>(A, act, stream);
+  } else {
+    if (wider)
+      launch_down<WB, 2, DW, 2, false>(A, act, stream);
+    else
+      launch_down<WB, 2, DW, 1, false>(A, act, stream);
+  }
+  decode_combine<<<dim3((unsigned)((A.H / 4 + CT - 1) / CT), A.T), CT, 0, stream>>>(A);
   return hipGetLastError();
 }
 
@@ -548,23 +731,20 @@ int decode_col_tiles(int64_t H, bool fp8) {
 
 hipError_t launch_router(const uint16_t* x, const void* wr, bool wr_f32, int T, int64_t H, int E, int K, bool renorm,
                          double* logits, int32_t* ids, float* weights, hipStream_t stream) {
-  const dim3 grid((E + GE - 1) / GE, (T + GT - 1) / GT);
   if (wr_f32)
-    router_logits<float><<<grid, GTHR, 0, stream>>>(x, (const float*)wr, T, H, E, logits);
+    launch_logits(x, (const float*)wr, T, H, E, logits, stream);
   else
-    router_logits<uint16_t><<<grid, GTHR, 0, stream>>>(x, (const uint16_t*)wr, T, H, E, logits);
-  router_topk<<<T, 64, 0, stream>>>(logits, E, K, renorm, ids, weights);
+    launch_logits(x, (const uint16_t*)wr, T, H, E, logits, stream);
+  if (E <= 128)
+    router_topk<128><<<T, 128, 0, stream>>>(logits, E, K, renorm, ids, weights);
+  else
+    router_topk<MAX_EXPERTS><<<T, MAX_EXPERTS, 0, stream>>>(logits, E, K, renorm, ids, weights);
   return hipGetLastError();
 }
 
 hipError_t launch_moe_decode(const DecodeArgs& A, bool fp8, hipStream_t stream) {
-  // an expert has at most T rows: T / 16 row tiles.  Four of them on bf16 weights
-  // hold 128 accumulator registers: four waves a workgroup, one a SIMD.
-  if (A.T <= 16)
-    return fp8 ? launch_experts<Fp8Weights<128>, 1, 8>(A, stream) : launch_experts<Bf16Weights, 1, 8>(A, stream);
-  if (A.T <= 32)
-    return fp8 ? launch_experts<Fp8Weights<128>, 2, 8>(A, stream) : launch_experts<Bf16Weights, 2, 8>(A, stream);
-  return fp8 ? launch_experts<Fp8Weights<64>, 4, 8>(A, stream) : launch_experts<Bf16Weights, 4, 4>(A, stream);
+  return fp8 ? launch_experts<Fp8Weights<128>, Fp8Weights<64>, 4>(A, stream)
+             : launch_experts<Bf16Weights, Bf16Weights, 4>(A, stream);
 }
 
 }  // namespace hmm

@@ -4,26 +4,23 @@ Argument marshalling only; the kernels are those of csrc/decode.hip behind hmm_m
 """
 
 import ctypes
+import functools
 
 import torch
 
 from . import _lib
-from .moe import _aligned, _ptr, _stream
+from ._bind import check_tensor, on_device, ptr, ready, stream_of
 
-MAX_TOKENS = 64
+_BF16 = (torch.bfloat16,)
 
 
-def _tensor(name, t, device, dtypes, dims):
-    if not isinstance(t, torch.Tensor):
-        raise TypeError("%s must be a torch.Tensor" % name)
-    if t.device.type != "cuda":
-        raise ValueError("%s must be on a HIP device (got %s)" % (name, t.device))
-    if device is not None and t.device != device:
-        raise ValueError("%s is on %s, x on %s" % (name, t.device, device))
-    if t.dtype not in dtypes:
-        raise TypeError("%s must be %s (got %s)" % (name, " or ".join(str(d) for d in dtypes), t.dtype))
-    if t.dim() != dims:
-        raise ValueError("%s must have %d dimensions (got %s)" % (name, dims, tuple(t.shape)))
+@functools.lru_cache(maxsize=256)
+def _problem(T, H, I, E, K, weight_dtype, router_dtype, flags):
+    """(problem, workspace bytes)"""
+    p = _lib.DecodeProblem(T, H, I, E, K, weight_dtype, router_dtype, flags)
+    n = ctypes.c_size_t()
+    _lib.check(_lib.load().hmm_moe_decode_sizes(ctypes.byref(p), ctypes.byref(n)))
+    return p, n.value
 
 
 def moe_decode(x, up_proj_weight, down_proj_weight, *, topk_ids=None, topk_weights=None, router_weight=None, top_k=None,
@@ -39,19 +36,19 @@ def moe_decode(x, up_proj_weight, down_proj_weight, *, topk_ids=None, topk_weigh
     [E,H/128,I/128] that quantize_block makes of them.  The weights must be contiguous: nothing of their size is
     copied.  For more tokens use hyper_mega_moe.
     """
-    _tensor("x", x, None, (torch.bfloat16,), 2)
+    check_tensor("x", x, _BF16, (2,))
     T, H = x.shape
     dev = x.device
     fp8 = up_descale is not None or down_descale is not None
     if fp8 and (up_descale is None or down_descale is None):
         raise ValueError("up_descale and down_descale go together")
-    wt = (torch.uint8,) if fp8 else (torch.bfloat16,)
-    _tensor("up_proj_weight", up_proj_weight, dev, wt, 3)
-    _tensor("down_proj_weight", down_proj_weight, dev, wt, 3)
+    wt = (torch.uint8,) if fp8 else _BF16
+    check_tensor("up_proj_weight", up_proj_weight, wt, (3,), dev)
+    check_tensor("down_proj_weight", down_proj_weight, wt, (3,), dev)
     E = up_proj_weight.shape[0]
     I = down_proj_weight.shape[2 if fp8 else 1]
     up, down = ((E, 2 * I, H), (E, H, I)) if fp8 else ((E, H, 2 * I), (E, I, H))
-    if tuple(up_proj_weight.shape) != up or tuple(down_proj_weight.shape) != down:
+    if up_proj_weight.shape != up or down_proj_weight.shape != down:
         raise ValueError("up_proj_weight and down_proj_weight must be %s (got %s, %s, H=%d)"
                          % ("[E,2I,H] and [E,H,I]" if fp8 else "[E,H,2I] and [E,I,H]", tuple(up_proj_weight.shape),
                             tuple(down_proj_weight.shape), H))
@@ -60,54 +57,53 @@ def moe_decode(x, up_proj_weight, down_proj_weight, *, topk_ids=None, topk_weigh
     if fp8:
         for name, t, shape in (("up_descale", up_descale, (E, 2 * I // 128, H // 128)),
                                ("down_descale", down_descale, (E, H // 128, I // 128))):
-            _tensor(name, t, dev, (torch.float32,), 3)
-            if tuple(t.shape) != shape:
+            check_tensor(name, t, (torch.float32,), (3,), dev)
+            if t.shape != shape:
                 raise ValueError("%s must be %s (got %s)" % (name, shape, tuple(t.shape)))
     routed = router_weight is not None
+    rdt = _lib.HMM_BF16
     if routed:
         if topk_ids is not None or topk_weights is not None:
             raise ValueError("give router_weight and top_k, or topk_ids and topk_weights")
         if not isinstance(top_k, int) or isinstance(top_k, bool):
             raise TypeError("top_k must be an int (got %r)" % (top_k,))
         K = top_k
-        _tensor("router_weight", router_weight, dev, (torch.bfloat16, torch.float32), 2)
-        if tuple(router_weight.shape) != (E, H):
+        check_tensor("router_weight", router_weight, (torch.bfloat16, torch.float32), (2,), dev)
+        if router_weight.shape != (E, H):
             raise ValueError("router_weight must be [E,H] = %s (got %s)" % ((E, H), tuple(router_weight.shape)))
+        if K > E:
+            raise ValueError("top_k = %d experts a token of E = %d" % (K, E))
+        if router_weight.dtype == torch.float32:
+            rdt = _lib.HMM_F32
     else:
         if topk_ids is None or topk_weights is None or top_k is not None:
             raise ValueError("give router_weight and top_k, or topk_ids and topk_weights")
-        _tensor("topk_ids", topk_ids, dev, (torch.int32, torch.int64), 2)
-        _tensor("topk_weights", topk_weights, dev, (torch.float32, torch.bfloat16, torch.float16, torch.float64), 2)
+        check_tensor("topk_ids", topk_ids, (torch.int32, torch.int64), (2,), dev)
+        check_tensor("topk_weights", topk_weights, (torch.float32, torch.bfloat16, torch.float16, torch.float64), (2,), dev)
         if topk_ids.shape[0] != T or topk_weights.shape != topk_ids.shape:
             raise ValueError("topk_ids and topk_weights must both be [T,K] with T = %d (got %s, %s)"
                              % (T, tuple(topk_ids.shape), tuple(topk_weights.shape)))
         K = topk_ids.shape[1]
-    rdt = _lib.HMM_F32 if routed and router_weight.dtype == torch.float32 else _lib.HMM_BF16
-    prob = _lib.DecodeProblem(T, H, I, E, K, _lib.HMM_FP8_E4M3_BLOCK if fp8 else _lib.HMM_BF16, rdt,
-                              _lib.HMM_DECODE_RENORMALIZE if renormalize else 0)
     if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (
             x, up_proj_weight, down_proj_weight, router_weight, topk_weights, up_descale, down_descale)):
         raise ValueError("moe_decode has no gradient: use hyper_mega_moe, or call it under torch.no_grad()")
-    lib = _lib.load()
-    ws = ctypes.c_size_t()
-    _lib.check(lib.hmm_moe_decode_sizes(ctypes.byref(prob), ctypes.byref(ws)))
-    if routed and K > E:
-        raise ValueError("top_k = %d experts a token of E = %d" % (K, E))
-    with torch.cuda.device(dev):
-        x_ = _aligned(x)
-        wr = _aligned(router_weight) if routed else None
-        if routed:
-            ids = torch.empty((T, K), dtype=torch.int32, device=dev)
-            w = torch.empty((T, K), dtype=torch.float32, device=dev)
-        else:
-            if topk_ids.dtype == torch.int64:  # an id past 32 bits must not wrap into range
-                topk_ids = topk_ids.clamp(-1, E)
-            ids, w = _aligned(topk_ids, torch.int32), _aligned(topk_weights, torch.float32)
-        ud, dd = (_aligned(up_descale), _aligned(down_descale)) if fp8 else (None, None)
-        y = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
-        if T > 0:
-            work = torch.empty(ws.value, dtype=torch.uint8, device=dev)
-            _lib.check(lib.hmm_moe_decode(ctypes.byref(prob), _ptr(x_), _ptr(wr), _ptr(ids), _ptr(w), _ptr(up_proj_weight),
-                                          _ptr(ud), _ptr(down_proj_weight), _ptr(dd), _ptr(y), _ptr(work), ws.value,
-                                          _stream(dev)))
+    prob, nbytes = _problem(T, H, I, E, K, _lib.HMM_FP8_E4M3_BLOCK if fp8 else _lib.HMM_BF16, rdt,
+                            _lib.HMM_DECODE_RENORMALIZE if renormalize else 0)
+    x = ready(x)
+    if routed:
+        wr = ready(router_weight)
+        ids = torch.empty((T, K), dtype=torch.int32, device=dev)
+        w = torch.empty((T, K), dtype=torch.float32, device=dev)
+    else:
+        wr = None
+        if topk_ids.dtype == torch.int64:  # an id past 32 bits must not wrap into range
+            topk_ids = topk_ids.clamp(-1, E)
+        ids, w = ready(topk_ids, torch.int32), ready(topk_weights, torch.float32)
+    ud, dd = (ready(up_descale), ready(down_descale)) if fp8 else (None, None)
+    y = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+    if T > 0:
+        work = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        with on_device(dev):
+            _lib.check(_lib.load().hmm_moe_decode(prob, ptr(x), ptr(wr), ptr(ids), ptr(w), ptr(up_proj_weight), ptr(ud),
+                                                  ptr(down_proj_weight), ptr(dd), ptr(y), ptr(work), nbytes, stream_of(dev)))
     return (y, ids, w) if routed else y

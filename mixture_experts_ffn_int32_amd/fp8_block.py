@@ -6,27 +6,16 @@ hmm_quant_block, hmm_matmul_fp8_block, hmm_linear_fp8_block and hmm_linear_fp8_b
 """
 
 import ctypes
+import functools
 
 import torch
 from torch.autograd.function import once_differentiable
 
 from . import _lib
-from .moe import _aligned, _ptr, _stream
+from ._bind import check_tensor, on_device, ptr, ready, stream_of
 
 GROUP = 128
-
-
-def _tensor(name, t, dtype, dims, device=None):
-    if not isinstance(t, torch.Tensor):
-        raise TypeError("%s must be a torch.Tensor" % name)
-    if t.device.type != "cuda":
-        raise ValueError("%s must be on a HIP device (got %s)" % (name, t.device))
-    if device is not None and t.device != device:
-        raise ValueError("%s is on %s, not on %s" % (name, t.device, device))
-    if t.dtype != dtype:
-        raise TypeError("%s must be %s (got %s)" % (name, dtype, t.dtype))
-    if t.dim() not in dims:
-        raise ValueError("%s must have %s dimensions (got %s)" % (name, " or ".join(map(str, dims)), tuple(t.shape)))
+_BF16, _U8, _F32 = (torch.bfloat16,), (torch.uint8,), (torch.float32,)
 
 
 def _widths(H, N, step):
@@ -41,7 +30,7 @@ def _quant(w, both):
     qt = torch.empty((E, N, H), dtype=torch.uint8, device=dev)
     q = torch.empty((E, H, N), dtype=torch.uint8, device=dev) if both else None
     ds = torch.empty((E, (N + GROUP - 1) // GROUP, H // GROUP), dtype=torch.float32, device=dev)
-    _lib.check(_lib.load().hmm_quant_block(_ptr(w), E, H, N, _ptr(qt), _ptr(q), _ptr(ds), _stream(dev)))
+    _lib.check(_lib.load().hmm_quant_block(ptr(w), E, H, N, ptr(qt), ptr(q), ptr(ds), stream_of(dev)))
     return qt, q, ds
 
 
@@ -52,35 +41,35 @@ def quantize_block(w):
     Returns (codes uint8 [(E,) N, H], descale float32 [(E,) ceil(N/128), H/128]): the codes are transposed, so
     that the contraction is contiguous.  Per block, in float32: scale = 448 * (1 / max|block|) (1 for
     zeros), code = E4M3 of w * scale, descale = 1 / scale."""
-    _tensor("w", w, torch.bfloat16, (2, 3))
+    check_tensor("w", w, _BF16, (2, 3))
     _widths(w.shape[-2], w.shape[-1], 16)
     if w.dim() == 3 and w.shape[0] < 1:
         raise ValueError("w must hold at least one matrix (got %s)" % (tuple(w.shape),))
-    with torch.cuda.device(w.device):
-        qt, _, ds = _quant(_aligned(w.detach() if w.dim() == 3 else w.detach()[None]), False)
+    with on_device(w.device):
+        qt, _, ds = _quant(ready(w.detach() if w.dim() == 3 else w.detach()[None]), False)
     return (qt, ds) if w.dim() == 3 else (qt[0], ds[0])
 
 
 def quantize_rows_block(x):
     """The tokens' side: (codes uint8 [T,H], descale float32 [T,H/128]) of x bf16 [T,H], quantize_block's rule per token
     and group of 128, as linear_fp8_block applies it."""
-    _tensor("x", x, torch.bfloat16, (2,))
+    check_tensor("x", x, _BF16, (2,))
     T, H = x.shape
     _widths(GROUP, H, GROUP)
-    x = _aligned(x.detach())
+    x = ready(x.detach())
     q = torch.empty((T, H), dtype=torch.uint8, device=x.device)
     d = torch.empty((T, H // GROUP), dtype=torch.float32, device=x.device)
-    with torch.cuda.device(x.device):
-        _lib.check(_lib.load().hmm_quant_rows_block(_ptr(x), T, H, _ptr(q), _ptr(d), _stream(x.device)))
+    with on_device(x.device):
+        _lib.check(_lib.load().hmm_quant_rows_block(ptr(x), T, H, ptr(q), ptr(d), stream_of(x.device)))
     return q, d
 
 
 def _check_codes(codes, descale, H, device):
-    _tensor("codes", codes, torch.uint8, (2,), device)
-    _tensor("descale", descale, torch.float32, (2,), device)
+    check_tensor("codes", codes, _U8, (2,), device)
+    check_tensor("descale", descale, _F32, (2,), device)
     N = codes.shape[0]
     _widths(H, N, 16)
-    if codes.shape[1] != H or tuple(descale.shape) != ((N + GROUP - 1) // GROUP, H // GROUP):
+    if codes.shape[1] != H or descale.shape != ((N + GROUP - 1) // GROUP, H // GROUP):
         raise ValueError("codes must be [N,H] and descale [ceil(N/128),H/128] (got %s, %s, H=%d)"
                          % (tuple(codes.shape), tuple(descale.shape), H))
     return N
@@ -89,31 +78,37 @@ def _check_codes(codes, descale, H, device):
 def matmul_fp8_block(xq, xs, codes, descale):
     """y bf16 [T,N] of tokens (xq uint8 [T,H], xs float32 [T,H/128], as quantize_rows_block gives them) and a weight
     (codes uint8 [N,H], descale float32 [ceil(N/128),H/128], as quantize_block does)."""
-    _tensor("xq", xq, torch.uint8, (2,))
+    check_tensor("xq", xq, _U8, (2,))
     T, H = xq.shape
-    _tensor("xs", xs, torch.float32, (2,), xq.device)
+    check_tensor("xs", xs, _F32, (2,), xq.device)
     N = _check_codes(codes, descale, H, xq.device)
-    if tuple(xs.shape) != (T, H // GROUP):
+    if xs.shape != (T, H // GROUP):
         raise ValueError("xs must be [T,H/128] (got %s, T=%d, H=%d)" % (tuple(xs.shape), T, H))
     dev = xq.device
-    with torch.cuda.device(dev):
-        xq, xs, codes, descale = (_aligned(t) for t in (xq, xs, codes, descale))
+    with on_device(dev):
+        xq, xs, codes, descale = (ready(t) for t in (xq, xs, codes, descale))
         y = torch.empty((T, N), dtype=torch.bfloat16, device=dev)
-        _lib.check(_lib.load().hmm_matmul_fp8_block(_ptr(xq), _ptr(xs), _ptr(codes), _ptr(descale), T, H, N, _ptr(y),
-                                                    _stream(dev)))
+        _lib.check(_lib.load().hmm_matmul_fp8_block(ptr(xq), ptr(xs), ptr(codes), ptr(descale), T, H, N, ptr(y),
+                                                    stream_of(dev)))
     return y
+
+
+@functools.lru_cache(maxsize=256)
+def _sizes(T, H, N):
+    """Workspace bytes of the forward and of the gradient."""
+    fwd, grad = ctypes.c_size_t(), ctypes.c_size_t()
+    _lib.check(_lib.load().hmm_linear_fp8_block_sizes(T, H, N, ctypes.byref(fwd), ctypes.byref(grad)))
+    return fwd.value, grad.value
 
 
 def _linear(x, codes, descale, N):
     T, H = x.shape
     dev = x.device
     lib = _lib.load()
-    fwd, grad = ctypes.c_size_t(), ctypes.c_size_t()
-    _lib.check(lib.hmm_linear_fp8_block_sizes(T, H, N, ctypes.byref(fwd), ctypes.byref(grad)))
+    nbytes = _sizes(T, H, N)[0]
     y = torch.empty((T, N), dtype=torch.bfloat16, device=dev)
-    work = torch.empty(fwd.value, dtype=torch.uint8, device=dev) if fwd.value else None
-    _lib.check(lib.hmm_linear_fp8_block(_ptr(x), _ptr(codes), _ptr(descale), T, H, N, _ptr(y), _ptr(work), fwd.value,
-                                        _stream(dev)))
+    work = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    _lib.check(lib.hmm_linear_fp8_block(ptr(x), ptr(codes), ptr(descale), T, H, N, ptr(y), ptr(work), nbytes, stream_of(dev)))
     return y
 
 
@@ -122,8 +117,8 @@ class LinearFp8BlockFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, weight):
-        x_, w = _aligned(x), _aligned(weight)
-        with torch.cuda.device(x.device):
+        x_, w = ready(x), ready(weight)
+        with on_device(x.device):
             qt, q, ds = _quant(w[None], ctx.needs_input_grad[0])
             y = _linear(x_, qt, ds, w.shape[1])
         ctx.save_for_backward(x_ if ctx.needs_input_grad[1] else None, q, ds)
@@ -137,15 +132,14 @@ class LinearFp8BlockFunction(torch.autograd.Function):
         T, H, N = ctx.dims
         dev = dy.device
         lib = _lib.load()
-        with torch.cuda.device(dev):
-            dy = _aligned(dy, torch.bfloat16)
+        with on_device(dev):
+            dy = ready(dy, torch.bfloat16)
             dx = torch.empty((T, H), dtype=torch.bfloat16, device=dev) if q is not None else None
             dw = torch.empty((H, N), dtype=torch.bfloat16, device=dev) if x is not None else None
-            fwd, grad = ctypes.c_size_t(), ctypes.c_size_t()
-            _lib.check(lib.hmm_linear_fp8_block_sizes(T, H, N, ctypes.byref(fwd), ctypes.byref(grad)))
-            work = torch.empty(grad.value, dtype=torch.uint8, device=dev)
-            _lib.check(lib.hmm_linear_fp8_block_grad(_ptr(dy), _ptr(x), _ptr(q), _ptr(ds), T, H, N, _ptr(dx), _ptr(dw),
-                                                     _ptr(work), grad.value, _stream(dev)))
+            nbytes = _sizes(T, H, N)[1]
+            work = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+            _lib.check(lib.hmm_linear_fp8_block_grad(ptr(dy), ptr(x), ptr(q), ptr(ds), T, H, N, ptr(dx), ptr(dw),
+                                                     ptr(work), nbytes, stream_of(dev)))
         return dx, dw
 
 
@@ -157,10 +151,10 @@ def linear_fp8_block(x, weight):
     both, dx from the E4M3 codes of dy (per token and 128 of N) and of the weight, dw = x^T dy as a bf16 product, the
     quantisation's own derivative taken as 1.  Or a pair (codes, descale) from quantize_block (serving; N a multiple
     of 16): no gradient.  At most 64 tokens of a quantised weight take one launch."""
-    _tensor("x", x, torch.bfloat16, (2,))
+    check_tensor("x", x, _BF16, (2,))
     H = x.shape[1]
     if isinstance(weight, torch.Tensor):
-        _tensor("weight", weight, torch.bfloat16, (2,), x.device)
+        check_tensor("weight", weight, _BF16, (2,), x.device)
         if weight.shape[0] != H:
             raise ValueError("weight must be [H,N] with H = %d (got %s)" % (H, tuple(weight.shape)))
         _widths(H, weight.shape[1], GROUP)
@@ -171,5 +165,5 @@ def linear_fp8_block(x, weight):
     N = _check_codes(codes, descale, H, x.device)
     if torch.is_grad_enabled() and x.requires_grad:
         raise ValueError("a quantised weight has no gradient: give the bf16 weight, or call under torch.no_grad()")
-    with torch.cuda.device(x.device):
-        return _linear(_aligned(x), _aligned(codes), _aligned(descale), N)
+    with on_device(x.device):
+        return _linear(ready(x), ready(codes), ready(descale), N)

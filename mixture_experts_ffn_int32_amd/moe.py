@@ -111,12 +111,6 @@ def _contig(t, dtype=None):
     return t.contiguous()
 
 
-def _aligned(t, dtype=None):
-    """_contig, and a copy of a view that does not start on 16 bytes (for small arguments: ids, weights, gates)."""
-    t = _contig(t, dtype)
-    return t.clone(memory_format=torch.contiguous_format) if t.data_ptr() % 16 else t
-
-
 def _forward_raw(x, ids, w, W1, W2, T, H, I, E, K, flags, gmm1=_lib.HMM_BF16, out=_lib.HMM_BF16, Ws1=None, Ws2=None):
     lib = _lib.load()
     Is = 0 if Ws2 is None else Ws2.shape[0]
