@@ -259,8 +259,6 @@ struct BlockTile {
   static_assert(BM * 8 % NTHR == 0 && BN * 8 % NTHR == 0, "stage loads");
 };
 
-typedef __attribute__((address_space(3))) void lds_void;
-
 struct BlockArgs {
   const uint8_t *xq, *wq;
   const float *xs, *ws;
@@ -270,17 +268,41 @@ struct BlockArgs {
   int mt, nt;
 };
 
-template <int ROWS, int NTHR>
-__device__ __forceinline__ void stage_rows(rsrc_t r, uint8_t* lds, uint32_t pitch, uint32_t koff) {
-  const int tid = threadIdx.x;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-#pragma unroll
-  for (int i = 0; i < ROWS * 8 / NTHR; ++i) {
-    const int row = (i * NTHR + tid) >> 3, pos = tid & 7;
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(lds + (i * NTHR + wave * 64) * 16), 16,
-                                             (int)((uint32_t)row * pitch + (uint32_t)((pos ^ (row & 7)) * 16)), (int)koff, 0, 0);
-  }
+// the words of make_rsrc's buffer resource, for assembly
+__device__ __forceinline__ u32x4 rsrc_words(const void* base, int64_t bytes) {
+  const uint64_t p = (uint64_t)base;
+  return u32x4{(uint32_t)__builtin_amdgcn_readfirstlane((int)p), (uint32_t)__builtin_amdgcn_readfirstlane((int)(p >> 32)),
+               (uint32_t)__builtin_amdgcn_readfirstlane((int)bytes), 0x00020000u};
 }
+
+// 16 bytes per lane from global memory to LDS at lds + 16 lane (lds: uniform).  Written in
+// assembly because the compiler, which cannot tell the two stages apart, would wait for a
+// load of the next stage before every read of this one; it has no register to return, and
+// the kernel waits for it itself (vmcnt) before the barrier that publishes the stage.
+__device__ __forceinline__ void load_lds16(u32x4 r, uint32_t lds, uint32_t voff, uint32_t soff) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+               :
+               : "s"(lds), "v"(voff), "s"(r), "s"(soff)
+               : "memory");
+}
+
+// ROWS rows of a stage: voff[i] is this lane's global offset of its i-th chunk
+template <int ROWS, int NTHR>
+struct StageRows {
+  static constexpr int N = ROWS * 8 / NTHR;
+  uint32_t voff[N];
+  __device__ __forceinline__ void init(uint32_t pitch) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int row = (i * NTHR + (int)threadIdx.x) >> 3, pos = threadIdx.x & 7;
+      voff[i] = (uint32_t)row * pitch + (uint32_t)((pos ^ (row & 7)) * 16);
+    }
+  }
+  __device__ __forceinline__ void load(u32x4 r, uint32_t lds, uint32_t koff, int wave) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) load_lds16(r, lds + (uint32_t)(i * NTHR + wave * 64) * 16, voff[i], koff);
+  }
+};
 
 __device__ __forceinline__ i32x8 frag(const uint8_t* base, int row, int kk, int half) {
   const int c = 4 * kk + half;
@@ -303,8 +325,8 @@ __global__ void __launch_bounds__(C::NTHR) block_gemm(const BlockArgs A) {
   const int wm = wave / C::WN, wn = wave % C::WN;
   const int half = lane >> 5, l32 = lane & 31;
   const uint32_t pitch = (uint32_t)A.H;
-  const rsrc_t rx = make_rsrc(A.xq + m0 * A.H, min((int64_t)C::BM, A.T - m0) * A.H);
-  const rsrc_t rw = make_rsrc(A.wq + n0 * A.H, min((int64_t)C::BN, A.N - n0) * A.H);
+  const u32x4 rx = rsrc_words(A.xq + m0 * A.H, min((int64_t)C::BM, A.T - m0) * A.H);
+  const u32x4 rw = rsrc_words(A.wq + n0 * A.H, min((int64_t)C::BN, A.N - n0) * A.H);
   const int groups = (int)(A.H / G);
   const float* xsp[C::MB];
 #pragma unroll
@@ -319,45 +341,63 @@ __global__ void __launch_bounds__(C::NTHR) block_gemm(const BlockArgs A) {
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[nb][mb][r] = 0.f;
 
-  auto stage = [&](int g, int buf) {
-    uint8_t* s = smem + buf * C::STAGE;
-    stage_rows<C::BN, C::NTHR>(rw, s, pitch, (uint32_t)g * G);
-    stage_rows<C::BM, C::NTHR>(rx, s + C::BN * G, pitch, (uint32_t)g * G);
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)smem;
+  StageRows<C::BN, C::NTHR> ldw;
+  StageRows<C::BM, C::NTHR> ldx;
+  ldw.init(pitch);
+  ldx.init(pitch);
+  auto stage = [&](int g) {
+    const uint32_t at = lds0 + (uint32_t)(g & 1) * C::STAGE;
+    ldw.load(rw, at, (uint32_t)g * G, wave);
+    ldx.load(rx, at + C::BN * G, (uint32_t)g * G, wave);
   };
   float xs[C::MB];
 #pragma unroll
   for (int mb = 0; mb < C::MB; ++mb) xs[mb] = xsp[mb][0];
-  stage(0, 0);
+  float sw = wsp[0];
+  stage(0);
+  constexpr int TILES = C::NB * C::MB;
   for (int g = 0; g < groups; ++g) {
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();  // stage g has landed for every wave, and every wave is done with stage g - 1
-    const float sw = wsp[(int64_t)g * A.ws_g];
+    asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");  // stage g has landed, stage g - 1 is done with
+    // the scales were loaded a step ahead: used here, before the next loads go out, they cost no wait
     float s[C::MB];
 #pragma unroll
     for (int mb = 0; mb < C::MB; ++mb) s[mb] = xs[mb] * sw;
+    __builtin_amdgcn_sched_barrier(0);
     if (g + 1 < groups) {
-      stage(g + 1, (g + 1) & 1);
 #pragma unroll
       for (int mb = 0; mb < C::MB; ++mb) xs[mb] = xsp[mb][g + 1];
+      sw = wsp[(int64_t)(g + 1) * A.ws_g];
+      stage(g + 1);
     }
     const uint8_t* sw_ = smem + (g & 1) * C::STAGE;
     const uint8_t* sx_ = sw_ + C::BN * G;
-    i32x8 fb[C::MB][2];
+    i32x8 fb[C::MB][2], fa[2][2];
 #pragma unroll
-    for (int mb = 0; mb < C::MB; ++mb)
+    for (int kk = 0; kk < 2; ++kk) {
+      fa[0][kk] = frag(sw_, wn * C::TN + l32, kk, half);
 #pragma unroll
-      for (int kk = 0; kk < 2; ++kk) fb[mb][kk] = frag(sx_, wm * C::TM + mb * 32 + l32, kk, half);
+      for (int mb = 0; mb < C::MB; ++mb) fb[mb][kk] = frag(sx_, wm * C::TM + mb * 32 + l32, kk, half);
+    }
+    // the matrix instructions of tile i run while the sums of tile i - 1 are scaled and added
+    f32x16 t[2];
 #pragma unroll
-    for (int nb = 0; nb < C::NB; ++nb) {
-      const i32x8 a0 = frag(sw_, wn * C::TN + nb * 32 + l32, 0, half);
-      const i32x8 a1 = frag(sw_, wn * C::TN + nb * 32 + l32, 1, half);
+    for (int i = 0; i <= TILES; ++i) {
+      const int nb = i / C::MB, mb = i % C::MB;
+      if (i < TILES) {
+        if (mb == 0 && nb + 1 < C::NB)
 #pragma unroll
-      for (int mb = 0; mb < C::MB; ++mb) {
-        f32x16 t = {};
-        t = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a0, fb[mb][0], t, 0, 0, 0, 127, 0, 127);
-        t = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a1, fb[mb][1], t, 0, 0, 0, 127, 0, 127);
+          for (int kk = 0; kk < 2; ++kk) fa[(nb + 1) & 1][kk] = frag(sw_, wn * C::TN + (nb + 1) * 32 + l32, kk, half);
+        const f32x16 zero = {};
+        t[i & 1] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fa[nb & 1][0], fb[mb][0], zero, 0, 0, 0, 127, 0, 127);
+        t[i & 1] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fa[nb & 1][1], fb[mb][1], t[i & 1], 0, 0, 0, 127, 0, 127);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if (i > 0) {
+        const int pn = (i - 1) / C::MB, pm = (i - 1) % C::MB;
 #pragma unroll
-        for (int r = 0; r < 16; ++r) acc[nb][mb][r] = __builtin_fmaf(s[mb], t[r], acc[nb][mb][r]);
+        for (int r = 0; r < 16; ++r) acc[pn][pm][r] = __builtin_fmaf(s[pm], t[(i - 1) & 1][r], acc[pn][pm][r]);
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
   }
