@@ -244,9 +244,9 @@ __global__ void __launch_bounds__(RW * 64) block_rows(const uint16_t* __restrict
 
 // ------------------------------------------------------------------- many rows
 // BM tokens by BN columns a workgroup, one group of 128 a step, two stages of LDS filled
-// by loads that bypass the registers.  A row of a stage is 128 bytes; its 16-byte chunk c
-// sits at position c ^ (row % 8), so the 16-byte reads of 8 consecutive rows cover every
-// bank once.  (The loads write LDS in lane order, so the permutation is applied to the
+// by loads that bypass the registers.  A row of a stage is 128 bytes, half of the banks; its
+// 16-byte chunk c sits at position c ^ (row / 2 % 8), so the 16-byte reads of 16 consecutive
+// rows cover every bank once.  (The loads write LDS in lane order, so the permutation is applied to the
 // global address, inside one 128-byte line.)
 template <int BM_, int BN_, int WM_, int WN_>
 struct BlockTile {
@@ -256,7 +256,7 @@ struct BlockTile {
   static constexpr int LDO = BN + 8;  // output tile pitch, elements
   static constexpr int LDS = 2 * STAGE > BM * LDO * 2 ? 2 * STAGE : BM * LDO * 2;
   static_assert(TN <= G && G % TN == 0, "a wave's columns lie in one weight block");
-  static_assert(BM * 8 % NTHR == 0 && BN * 8 % NTHR == 0, "stage loads");
+  static_assert(BM * 8 % NTHR == 0 && BN * 8 % NTHR == 0, "whole loads a stage");
 };
 
 struct BlockArgs {
@@ -286,28 +286,10 @@ __device__ __forceinline__ void load_lds16(u32x4 r, uint32_t lds, uint32_t voff,
                : "memory");
 }
 
-// ROWS rows of a stage: voff[i] is this lane's global offset of its i-th chunk
-template <int ROWS, int NTHR>
-struct StageRows {
-  static constexpr int N = ROWS * 8 / NTHR;
-  uint32_t voff[N];
-  __device__ __forceinline__ void init(uint32_t pitch) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int row = (i * NTHR + (int)threadIdx.x) >> 3, pos = threadIdx.x & 7;
-      voff[i] = (uint32_t)row * pitch + (uint32_t)((pos ^ (row & 7)) * 16);
-    }
-  }
-  __device__ __forceinline__ void load(u32x4 r, uint32_t lds, uint32_t koff, int wave) const {
-#pragma unroll
-    for (int i = 0; i < N; ++i) load_lds16(r, lds + (uint32_t)(i * NTHR + wave * 64) * 16, voff[i], koff);
-  }
-};
-
 __device__ __forceinline__ i32x8 frag(const uint8_t* base, int row, int kk, int half) {
   const int c = 4 * kk + half;
-  const u32x4 lo = *reinterpret_cast<const u32x4*>(base + row * G + ((c ^ (row & 7)) * 16));
-  const u32x4 hi = *reinterpret_cast<const u32x4*>(base + row * G + (((c + 2) ^ (row & 7)) * 16));
+  const u32x4 lo = *reinterpret_cast<const u32x4*>(base + row * G + ((c ^ ((row >> 1) & 7)) * 16));
+  const u32x4 hi = *reinterpret_cast<const u32x4*>(base + row * G + (((c + 2) ^ ((row >> 1) & 7)) * 16));
   return i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
 }
 
@@ -342,20 +324,26 @@ __global__ void __launch_bounds__(C::NTHR) block_gemm(const BlockArgs A) {
       for (int r = 0; r < 16; ++r) acc[nb][mb][r] = 0.f;
 
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)smem;
-  StageRows<C::BN, C::NTHR> ldw;
-  StageRows<C::BM, C::NTHR> ldx;
-  ldw.init(pitch);
-  ldx.init(pitch);
-  auto stage = [&](int g) {
-    const uint32_t at = lds0 + (uint32_t)(g & 1) * C::STAGE;
-    ldw.load(rw, at, (uint32_t)g * G, wave);
-    ldx.load(rx, at + C::BN * G, (uint32_t)g * G, wave);
+  // A load takes 8 lanes a row, so the workgroup's i-th one starts RPL rows (a multiple of 16,
+  // the permutation's period) further: one offset register serves all of them, and both operands.
+  constexpr int RPL = C::NTHR / 8, LW = C::BN / RPL, LOADS = LW + C::BM / RPL;
+  static_assert(RPL % 16 == 0, "permutation period");
+  const uint32_t voff = (threadIdx.x >> 3) * pitch + (((threadIdx.x & 7) ^ ((threadIdx.x >> 4) & 7)) * 16);
+  // loads [from, to) of stage g (past the last one: of the last one again, unused).  Rows past the
+  // tensors' ends are beyond the resources and come back as zeros; the scalar offset stays inside.
+  auto stage = [&](int g, int from, int to) {
+    const uint32_t at = lds0 + (uint32_t)(g & 1) * C::STAGE + (uint32_t)wave * 1024;
+    const uint32_t koff = (uint32_t)min(g, groups - 1) * G;
+#pragma unroll
+    for (int i = from; i < to; ++i)
+      load_lds16(i < LW ? rw : rx, at + (uint32_t)i * C::NTHR * 16,
+                 voff + (uint32_t)(i < LW ? i : i - LW) * RPL * pitch, koff);
   };
   float xs[C::MB];
 #pragma unroll
   for (int mb = 0; mb < C::MB; ++mb) xs[mb] = xsp[mb][0];
   float sw = wsp[0];
-  stage(0);
+  stage(0, 0, LOADS);
   constexpr int TILES = C::NB * C::MB;
   for (int g = 0; g < groups; ++g) {
     asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");  // stage g has landed, stage g - 1 is done with
@@ -364,12 +352,10 @@ __global__ void __launch_bounds__(C::NTHR) block_gemm(const BlockArgs A) {
 #pragma unroll
     for (int mb = 0; mb < C::MB; ++mb) s[mb] = xs[mb] * sw;
     __builtin_amdgcn_sched_barrier(0);
-    if (g + 1 < groups) {
+    const int gn = min(g + 1, groups - 1);
 #pragma unroll
-      for (int mb = 0; mb < C::MB; ++mb) xs[mb] = xsp[mb][g + 1];
-      sw = wsp[(int64_t)(g + 1) * A.ws_g];
-      stage(g + 1);
-    }
+    for (int mb = 0; mb < C::MB; ++mb) xs[mb] = xsp[mb][gn];
+    sw = wsp[(int64_t)gn * A.ws_g];
     const uint8_t* sw_ = smem + (g & 1) * C::STAGE;
     const uint8_t* sx_ = sw_ + C::BN * G;
     i32x8 fb[C::MB][2], fa[2][2];
@@ -379,7 +365,9 @@ __global__ void __launch_bounds__(C::NTHR) block_gemm(const BlockArgs A) {
 #pragma unroll
       for (int mb = 0; mb < C::MB; ++mb) fb[mb][kk] = frag(sx_, wm * C::TM + mb * 32 + l32, kk, half);
     }
-    // the matrix instructions of tile i run while the sums of tile i - 1 are scaled and added
+    // The matrix instructions of tile i run while the sums of tile i - 1 are scaled and added;
+    // the next stage's loads go out one by one between them (all at once they would fill the
+    // address unit's queue, and each wave's later instructions wait behind its own).
     f32x16 t[2];
 #pragma unroll
     for (int i = 0; i <= TILES; ++i) {
@@ -392,6 +380,7 @@ __global__ void __launch_bounds__(C::NTHR) block_gemm(const BlockArgs A) {
         t[i & 1] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fa[nb & 1][0], fb[mb][0], zero, 0, 0, 0, 127, 0, 127);
         t[i & 1] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fa[nb & 1][1], fb[mb][1], t[i & 1], 0, 0, 0, 127, 0, 127);
         __builtin_amdgcn_sched_barrier(0);
+        stage(g + 1, i * LOADS / TILES, (i + 1) * LOADS / TILES);
       }
       if (i > 0) {
         const int pn = (i - 1) / C::MB, pm = (i - 1) % C::MB;
@@ -401,6 +390,7 @@ __global__ void __launch_bounds__(C::NTHR) block_gemm(const BlockArgs A) {
       }
     }
   }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the loads past the last stage write into LDS
   __syncthreads();
   // the tile in bf16 through LDS, so that stores are rows of 16-byte chunks
   uint16_t* out = reinterpret_cast<uint16_t*>(smem);
