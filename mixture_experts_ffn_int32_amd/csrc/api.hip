@@ -1443,7 +1443,7 @@ BlockWork block_work(int64_t rows, int64_t K) {
   w.total = w.xs + up((size_t)rows * (K / 128) * 4);
   return w;
 }
-size_t block_grad_bytes(int64_t T, int64_t N) { return block_work(T, N).total + up(8); }
+size_t block_grad_bytes(int64_t T, int64_t N) { return block_work(T, N).total; }
 }  // namespace
 
 extern "C" {
@@ -1526,12 +1526,12 @@ hmm_status hmm_linear_fp8_block_grad(const void* dy, const void* x, const uint8_
   const bool ne = T > 0;
   if ((s = need(dy, ne, "dy")) || (s = need(x, ne && dw, "x")) || (s = need(codes, ne && dx, "codes")) ||
       (s = need(descale, ne && dx, "descale")) || (s = need(dx, false, "dx")) || (s = need(dw, false, "dw")) ||
-      (s = need(workspace, ne, "workspace")))
+      (s = need(workspace, ne && dx, "workspace")))
     return s;
   // the weight gradient's product addresses each operand through one 4 GiB buffer
   if (dw && (T * H >= (int64_t)1 << 31 || T * N >= (int64_t)1 << 31))
     return fail(HMM_ERR_UNSUPPORTED, "x and dy must be below 4 GiB for the weight gradient");
-  if (workspace_bytes < block_grad_bytes(T, N))
+  if (dx && workspace_bytes < block_grad_bytes(T, N))
     return fail(HMM_ERR_WORKSPACE_TOO_SMALL, "workspace is %zu bytes, %zu needed", workspace_bytes, block_grad_bytes(T, N));
   hipStream_t st = (hipStream_t)stream;
   const BlockWork w = block_work(T, N);
@@ -1544,13 +1544,9 @@ hmm_status hmm_linear_fp8_block_grad(const void* dy, const void* x, const uint8_
     if (e != hipSuccess) return hip_fail(e, "FP8 block product launch");
   }
   if (dw) {
-    if (!workspace) return fail(HMM_ERR_NULL_POINTER, "workspace is NULL");
-    int32_t* offsets = at<int32_t>(workspace, w.total);
     Stage stage("linear_fp8_block_dw", st);
-    hipError_t e = hmm::launch_dense_offsets(offsets, T, st);
-    if (e != hipSuccess) return hip_fail(e, "offsets launch");
-    const hmm::DwJob job{offsets, nullptr, 1, (const uint16_t*)x, (const uint16_t*)dy, T, T, H, N, (uint16_t*)dw};
-    e = hmm::launch_dw_dense(job, ((H + 255) / 256) * ((N + 255) / 256) < 64, st);
+    const hmm::DwJob job{nullptr, nullptr, 1, (const uint16_t*)x, (const uint16_t*)dy, T, T, H, N, (uint16_t*)dw};
+    const hipError_t e = hmm::launch_dw_dense(job, st);
     if (e != hipSuccess) return hip_fail(e, "weight gradient launch");
   }
   return HMM_OK;

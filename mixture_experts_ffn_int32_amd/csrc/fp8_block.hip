@@ -243,20 +243,21 @@ __global__ void __launch_bounds__(RW * 64) block_rows(const uint16_t* __restrict
 }
 
 // ------------------------------------------------------------------- many rows
-// BM tokens by BN columns a workgroup, one group of 128 a step, two stages of LDS filled
-// by loads that bypass the registers.  A row of a stage is 128 bytes, half of the banks; its
+// BM tokens by BN columns a workgroup, one group of 128 a step, NS stages of LDS filled
+// by loads that bypass the registers (the tokens' scales among them).  A row of a stage is 128 bytes, half of the banks; its
 // 16-byte chunk c sits at position c ^ (row / 2 % 8), so the 16-byte reads of 16 consecutive
 // rows cover every bank once.  (The loads write LDS in lane order, so the permutation is applied to the
 // global address, inside one 128-byte line.)
-template <int BM_, int BN_, int WM_, int WN_>
+template <int BM_, int BN_, int WM_, int WN_, int NS_>
 struct BlockTile {
-  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NTHR = WM * WN * 64;
+  static constexpr int SPREAD = 4;
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NS = NS_, NTHR = WM * WN * 64;
   static constexpr int TM = BM / WM, TN = BN / WN, MB = TM / 32, NB = TN / 32;
-  static constexpr int STAGE = (BM + BN) * G;
+  static constexpr int STAGE = (BM + BN) * G + BM * 4;  // weight rows, token rows, token scales
   static constexpr int LDO = BN + 8;  // output tile pitch, elements
-  static constexpr int LDS = 2 * STAGE > BM * LDO * 2 ? 2 * STAGE : BM * LDO * 2;
+  static constexpr int LDS = NS * STAGE > BM * LDO * 2 ? NS * STAGE : BM * LDO * 2;
   static_assert(TN <= G && G % TN == 0, "a wave's columns lie in one weight block");
-  static_assert(BM * 8 % NTHR == 0 && BN * 8 % NTHR == 0, "whole loads a stage");
+  static_assert(BM * 8 % NTHR == 0 && BN * 8 % NTHR == 0 && BM % 64 == 0 && NTHR % BM == 0, "whole loads a stage");
 };
 
 struct BlockArgs {
@@ -281,6 +282,13 @@ __device__ __forceinline__ u32x4 rsrc_words(const void* base, int64_t bytes) {
 // the kernel waits for it itself (vmcnt) before the barrier that publishes the stage.
 __device__ __forceinline__ void load_lds16(u32x4 r, uint32_t lds, uint32_t voff, uint32_t soff) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+               :
+               : "s"(lds), "v"(voff), "s"(r), "s"(soff)
+               : "memory");
+}
+// the same of 4 bytes per lane
+__device__ __forceinline__ void load_lds4(u32x4 r, uint32_t lds, uint32_t voff, uint32_t soff) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds"
                :
                : "s"(lds), "v"(voff), "s"(r), "s"(soff)
                : "memory");
@@ -310,9 +318,7 @@ __global__ void __launch_bounds__(C::NTHR) block_gemm(const BlockArgs A) {
   const u32x4 rx = rsrc_words(A.xq + m0 * A.H, min((int64_t)C::BM, A.T - m0) * A.H);
   const u32x4 rw = rsrc_words(A.wq + n0 * A.H, min((int64_t)C::BN, A.N - n0) * A.H);
   const int groups = (int)(A.H / G);
-  const float* xsp[C::MB];
-#pragma unroll
-  for (int mb = 0; mb < C::MB; ++mb) xsp[mb] = A.xs + min(m0 + wm * C::TM + mb * 32 + l32, A.T - 1) * groups;
+  const u32x4 rs = rsrc_words(A.xs + m0 * groups, min((int64_t)C::BM, A.T - m0) * groups * 4);
   const float* wsp = A.ws + ((n0 + wn * C::TN) / G < (A.N + G - 1) / G ? (n0 + wn * C::TN) / G : 0) * A.ws_n;
 
   f32x16 acc[C::NB][C::MB];
@@ -329,35 +335,38 @@ __global__ void __launch_bounds__(C::NTHR) block_gemm(const BlockArgs A) {
   constexpr int RPL = C::NTHR / 8, LW = C::BN / RPL, LOADS = LW + C::BM / RPL;
   static_assert(RPL % 16 == 0, "permutation period");
   const uint32_t voff = (threadIdx.x >> 3) * pitch + (((threadIdx.x & 7) ^ ((threadIdx.x >> 4) & 7)) * 16);
-  // loads [from, to) of stage g (past the last one: of the last one again, unused).  Rows past the
-  // tensors' ends are beyond the resources and come back as zeros; the scalar offset stays inside.
-  auto stage = [&](int g, int from, int to) {
-    const uint32_t at = lds0 + (uint32_t)(g & 1) * C::STAGE + (uint32_t)wave * 1024;
-    const uint32_t koff = (uint32_t)min(g, groups - 1) * G;
+  const uint32_t soff = (uint32_t)(threadIdx.x % C::BM) * (uint32_t)groups * 4;
+  // Loads [from, to) of stage g into its buffer (past the last stage: of the last one again,
+  // unused); the last of them is the scales', 64 tokens a wave.  Rows past the tensors' ends are
+  // beyond the resources and come back as zeros; the scalar offset stays inside.
+  auto stage = [&](int g, int buf, int from, int to) {
+    const uint32_t at = lds0 + (uint32_t)buf * C::STAGE;
+    const int gc = min(g, groups - 1);
 #pragma unroll
     for (int i = from; i < to; ++i)
-      load_lds16(i < LW ? rw : rx, at + (uint32_t)i * C::NTHR * 16,
-                 voff + (uint32_t)(i < LW ? i : i - LW) * RPL * pitch, koff);
+      if (i < LOADS)
+        load_lds16(i < LW ? rw : rx, at + (uint32_t)(i * C::NTHR + wave * 64) * 16,
+                   voff + (uint32_t)(i < LW ? i : i - LW) * RPL * pitch, (uint32_t)gc * G);
+      else
+        load_lds4(rs, at + (C::BM + C::BN) * G + (uint32_t)(wave % (C::BM / 64)) * 256, soff, (uint32_t)gc * 4);
   };
-  float xs[C::MB];
+  constexpr int TILES = C::NB * C::MB, ALL = LOADS + 1, PER = (ALL + (C::SPREAD < TILES ? C::SPREAD : TILES) - 1) / (C::SPREAD < TILES ? C::SPREAD : TILES);
 #pragma unroll
-  for (int mb = 0; mb < C::MB; ++mb) xs[mb] = xsp[mb][0];
-  float sw = wsp[0];
-  stage(0, 0, LOADS);
-  constexpr int TILES = C::NB * C::MB;
+  for (int q = 0; q < C::NS - 1; ++q) stage(q, q, 0, ALL);
+  // the block's scales: lane l holds that of group g0 + l, reloaded every 64 groups
+  float wl = 0.f;
+  int buf = 0, fill = C::NS - 1;
   for (int g = 0; g < groups; ++g) {
-    asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");  // stage g has landed, stage g - 1 is done with
-    // the scales were loaded a step ahead: used here, before the next loads go out, they cost no wait
-    float s[C::MB];
-#pragma unroll
-    for (int mb = 0; mb < C::MB; ++mb) s[mb] = xs[mb] * sw;
-    __builtin_amdgcn_sched_barrier(0);
-    const int gn = min(g + 1, groups - 1);
-#pragma unroll
-    for (int mb = 0; mb < C::MB; ++mb) xs[mb] = xsp[mb][gn];
-    sw = wsp[(int64_t)gn * A.ws_g];
-    const uint8_t* sw_ = smem + (g & 1) * C::STAGE;
+    if ((g & 63) == 0) {
+      wl = wsp[(int64_t)min(g + lane, groups - 1) * A.ws_g];
+      asm volatile("" : "+v"(wl));  // waits for it here, once in 64 steps
+    }
+    // stage g has landed (NS - 2 later ones may be on their way), and stage g - 1 is done with
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"i"((C::NS - 2) * ALL) : "memory");
+    const float sw = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, wl), g & 63));
+    const uint8_t* sw_ = smem + buf * C::STAGE;
     const uint8_t* sx_ = sw_ + C::BN * G;
+    const float* ss_ = reinterpret_cast<const float*>(sx_ + C::BM * G);
     i32x8 fb[C::MB][2], fa[2][2];
 #pragma unroll
     for (int kk = 0; kk < 2; ++kk) {
@@ -365,6 +374,9 @@ __global__ void __launch_bounds__(C::NTHR) block_gemm(const BlockArgs A) {
 #pragma unroll
       for (int mb = 0; mb < C::MB; ++mb) fb[mb][kk] = frag(sx_, wm * C::TM + mb * 32 + l32, kk, half);
     }
+    float s[C::MB];
+#pragma unroll
+    for (int mb = 0; mb < C::MB; ++mb) s[mb] = ss_[wm * C::TM + mb * 32 + l32] * sw;
     // The matrix instructions of tile i run while the sums of tile i - 1 are scaled and added;
     // the next stage's loads go out one by one between them (all at once they would fill the
     // address unit's queue, and each wave's later instructions wait behind its own).
@@ -380,7 +392,7 @@ __global__ void __launch_bounds__(C::NTHR) block_gemm(const BlockArgs A) {
         t[i & 1] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fa[nb & 1][0], fb[mb][0], zero, 0, 0, 0, 127, 0, 127);
         t[i & 1] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fa[nb & 1][1], fb[mb][1], t[i & 1], 0, 0, 0, 127, 0, 127);
         __builtin_amdgcn_sched_barrier(0);
-        stage(g + 1, i * LOADS / TILES, (i + 1) * LOADS / TILES);
+        stage(g + C::NS - 1, fill, min(i * PER, ALL), min((i + 1) * PER, ALL));
       }
       if (i > 0) {
         const int pn = (i - 1) / C::MB, pm = (i - 1) % C::MB;
@@ -389,6 +401,8 @@ __global__ void __launch_bounds__(C::NTHR) block_gemm(const BlockArgs A) {
         __builtin_amdgcn_sched_barrier(0);
       }
     }
+    buf = buf + 1 == C::NS ? 0 : buf + 1;
+    fill = fill + 1 == C::NS ? 0 : fill + 1;
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the loads past the last stage write into LDS
   __syncthreads();
@@ -432,11 +446,6 @@ hipError_t launch_rows(const uint16_t* x, const uint8_t* wq, const float* ws, in
   return hipGetLastError();
 }
 
-__global__ void dense_offsets(int32_t* offsets, int32_t T) {
-  offsets[0] = 0;
-  offsets[1] = T;
-}
-
 }  // namespace
 
 hipError_t launch_quant_block(const uint16_t* w, int64_t E, int64_t H, int64_t N, uint8_t* qt, uint8_t* q, float* ds,
@@ -466,14 +475,9 @@ hipError_t launch_block_gemm(const uint8_t* xq, const float* xs, const uint8_t* 
   const int groups = (int)(H / G), nbs = (int)((N + G - 1) / G);
   const BlockArgs a{xq, wq, xs, ws, T, H, N, ws_transposed ? 1 : groups, ws_transposed ? nbs : 1, y, 0, 0};
   const auto tiles = [&](int64_t bm, int64_t bn) { return ((T + bm - 1) / bm) * ((N + bn - 1) / bn); };
-  if (tiles(256, 256) >= 192) return launch_gemm<BlockTile<256, 256, 4, 2>>(a, stream);
-  if (tiles(128, 128) >= 192) return launch_gemm<BlockTile<128, 128, 2, 2>>(a, stream);
-  return launch_gemm<BlockTile<64, 64, 2, 2>>(a, stream);
-}
-
-hipError_t launch_dense_offsets(int32_t* offsets, int64_t T, hipStream_t stream) {
-  dense_offsets<<<1, 1, 0, stream>>>(offsets, (int32_t)T);
-  return hipGetLastError();
+  if (tiles(256, 256) >= 192) return launch_gemm<BlockTile<256, 256, 4, 2, 2>>(a, stream);
+  if (tiles(128, 128) >= 192) return launch_gemm<BlockTile<128, 128, 2, 2, 2>>(a, stream);
+  return launch_gemm<BlockTile<64, 64, 2, 2, 3>>(a, stream);
 }
 
 }  // namespace hmm

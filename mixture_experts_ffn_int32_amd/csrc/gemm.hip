@@ -341,9 +341,18 @@ hipError_t launch_dw2(const DwJob* jobs, int n, bool narrow, hipStream_t stream)
                 : launch_dw_jobs<Big, false, true>(jobs, n, stream);
 }
 
-hipError_t launch_dw_dense(const DwJob& job, bool narrow, hipStream_t stream) {
-  return narrow ? launch_dw_jobs<Narrow, false, false>(&job, 1, stream)
-                : launch_dw_jobs<Big, false, false>(&job, 1, stream);
+template <class C>
+static hipError_t launch_dw_dense_tiles(const DwJob& job, hipStream_t stream) {
+  const auto a = dw_args<C, false, false>(job);
+  return launch<Dw<C, false, false>>(a, dw_blocks(a), stream);
+}
+// The widest tiles that give (nearly) every CU one.  4096 rows, M = 4096, N = 2048: 256 x 256 tiles
+// (128 of them) 103 us, 256 x 128 73 us, 128 x 128 81 us, 64 x 64 136 us.
+hipError_t launch_dw_dense(const DwJob& job, hipStream_t stream) {
+  const auto tiles = [&](int64_t bm, int64_t bn) { return ((job.M + bm - 1) / bm) * ((job.N + bn - 1) / bn); };
+  if (tiles(256, 256) >= 192) return launch_dw_dense_tiles<Big>(job, stream);
+  if (tiles(256, 128) >= 128) return launch_dw_dense_tiles<Mid>(job, stream);
+  return launch_dw_dense_tiles<Narrow>(job, stream);
 }
 
 hipError_t launch_act_grad_dw2_narrow(const ActGradJob* ag, const DwJob* dw2, int n, hipStream_t stream) {

@@ -316,8 +316,13 @@ struct Dw : PlainCols<Cc> {
     raster(t, A.mt, A.nt, r, c);
     m0 = r * C::BM;
     n0 = c * C::BN;
-    p0 = A.offsets[e];
-    p1 = A.offsets[e + 1];
+    if constexpr (GATHER_A || GATHER_B) {
+      p0 = A.offsets[e];
+      p1 = A.offsets[e + 1];
+    } else {  // plain matrices: one group of all rows
+      p0 = 0;
+      p1 = (int)A.a_rows;
+    }
     nk = (p1 - p0 + C::BK - 1) / C::BK;
     ra_ = make_rsrc(A.A, A.a_rows * A.M * 2);
     rb_ = make_rsrc(A.B, A.b_rows * A.N * 2);

@@ -31,6 +31,7 @@ struct Cfg {
 typedef Cfg<256, 256, 2, 4> Big;
 typedef Cfg<64, 256, 2, 4> Small;
 typedef Cfg<64, 64, 2, 2> Narrow;
+typedef Cfg<256, 128, 4, 2> Mid;
 
 typedef __attribute__((address_space(3))) bf16x4 lds_bf16x4;
 

@@ -174,8 +174,8 @@ hipError_t launch_dw1(const DwJob* jobs, int n, bool narrow, hipStream_t stream)
 // for the weight gradients to start the longest reductions first (route.hip)
 hipError_t launch_expert_order(const int32_t* counts, int E, int32_t* order, hipStream_t stream);
 hipError_t launch_dw2(const DwJob* jobs, int n, bool narrow, hipStream_t stream);
-// C = A^T B of plain matrices (E = 1, offsets = {0, rows}; tok_of_row is not read)
-hipError_t launch_dw_dense(const DwJob& job, bool narrow, hipStream_t stream);
+// C = A^T B of plain matrices A [rows][M] and B [rows][N] (E = 1; offsets and tok_of_row are not read)
+hipError_t launch_dw_dense(const DwJob& job, hipStream_t stream);
 // Small problems (narrow tiles): the independent products share a launch,
 // act_grad with W2Grad, then input_grad with W1Grad (the same products as above;
 // with a shared expert, its two products join each launch).
@@ -357,6 +357,5 @@ hipError_t launch_block_rows(const uint16_t* x, const uint8_t* wq, const float* 
 //   y [T][N] of codes xq [T][H], xs [T][H/128]; ws [ceil(N/128)][H/128], or its transpose
 hipError_t launch_block_gemm(const uint8_t* xq, const float* xs, const uint8_t* wq, const float* ws, int64_t T, int64_t H,
                              int64_t N, bool ws_transposed, uint16_t* y, hipStream_t stream);
-hipError_t launch_dense_offsets(int32_t* offsets, int64_t T, hipStream_t stream);
 
 }  // namespace hmm

@@ -102,32 +102,85 @@ __device__ __forceinline__ void gate8(const NormArgs& A, int64_t t, int64_t i, f
 template <int NT>
 constexpr int rows_per_block() { return NT == 64 ? 4 : 1; }
 
-template <int NT, int V>
+// 8 elements as they were loaded: bf16, or float32 where F32
+template <bool F32>
+struct Raw8 {
+  u32x4 v[F32 ? 2 : 1];
+  __device__ __forceinline__ void load(const void* p, int64_t i) {
+    const u32x4* q = reinterpret_cast<const u32x4*>(static_cast<const char*>(p) + i * (F32 ? 4 : 2));
+#pragma unroll
+    for (int k = 0; k < (F32 ? 2 : 1); ++k) v[k] = q[k];
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int k = 0; k < (F32 ? 2 : 1); ++k) v[k] = u32x4{0, 0, 0, 0};
+  }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+    if constexpr (F32) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = __uint_as_float(v[j >> 2][j & 3]);
+    } else {
+      unpack8(v[0], f);
+    }
+  }
+};
+
+// RF, WF: the residual stream and the weights are float32.
+template <int NT, int V, bool RF, bool WF>
 __global__ void __launch_bounds__(NT == 64 ? 256 : NT) residual_norm_fwd(const NormArgs A) {
   constexpr int RPB = rows_per_block<NT>();
   __shared__ float lds[MAX_THREADS_PER_ROW / 64];
   const int tid = NT == 64 ? (threadIdx.x & 63) : threadIdx.x;
   const int slot = NT == 64 ? threadIdx.x >> 6 : 0;
   const float invH = 1.f / (float)A.H;
-  for (int64_t t = (int64_t)blockIdx.x * RPB + slot; t < A.T; t += (int64_t)gridDim.x * RPB) {
-    float r[V][8], y[V][8];
-    float sum[1] = {0.f};
+  Raw8<WF> w[V], wp[V];
+  // a row's data is loaded while the row before it is reduced and written
+  struct Row {
+    Raw8<RF> r[V];
+    Raw8<false> y[V];
+  };
+  auto load = [&](Row& R, int64_t t) {
 #pragma unroll
     for (int k = 0; k < V; ++k) {
       const int64_t i = (int64_t)(tid + k * NT) * 8;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) r[k][j] = y[k][j] = 0.f;
+      R.r[k].zero();
+      R.y[k].zero();
       if (i >= A.H) continue;
-      load8(A.residual, A.res_f32, t * A.H + i, r[k]);
-      if (A.y) load8(A.y, false, t * A.H + i, y[k]);
+      R.r[k].load(A.residual, t * A.H + i);
+      if (A.y) R.y[k].load(A.y, t * A.H + i);
     }
+  };
+  const int64_t step = (int64_t)gridDim.x * RPB;
+  int64_t t = (int64_t)blockIdx.x * RPB + slot;
+  Row R;
+  if (t < A.T) load(R, t);
+#pragma unroll
+  for (int k = 0; k < V; ++k) {
+    const int64_t i = (int64_t)(tid + k * NT) * 8;
+    w[k].zero();
+    wp[k].zero();
+    if (i >= A.H) continue;
+    w[k].load(A.norm_weight, i);
+    if (A.post_weight) wp[k].load(A.post_weight, i);
+  }
+  for (; t < A.T; t += step) {
+    Row N;
+    load(N, t + step < A.T ? t + step : t);
+    __builtin_amdgcn_sched_barrier(0);
+    float r[V][8];
+    float sum[1] = {0.f};
+#pragma unroll
+    for (int k = 0; k < V; ++k) R.r[k].get(r[k]);
     if (A.y) {
       float rho_y = 1.f;
       if (A.post_weight) {
 #pragma unroll
-        for (int k = 0; k < V; ++k)
+        for (int k = 0; k < V; ++k) {
+          float y[8];
+          R.y[k].get(y);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) sum[0] = __builtin_fmaf(y[k][j], y[k][j], sum[0]);
+          for (int j = 0; j < 8; ++j) sum[0] = __builtin_fmaf(y[j], y[j], sum[0]);
+        }
         row_sum<NT>(sum, lds);
         rho_y = rsqrt_(__builtin_fmaf(sum[0], invH, A.eps));
       }
@@ -136,19 +189,20 @@ __global__ void __launch_bounds__(NT == 64 ? 256 : NT) residual_norm_fwd(const N
       for (int k = 0; k < V; ++k) {
         const int64_t i = (int64_t)(tid + k * NT) * 8;
         if (i >= A.H) continue;
-        float g[8], wp[8];
+        float g[8], y[8], wpv[8];
         gate8(A, t, i, g);
+        R.y[k].get(y);
         if (A.post_weight) {
-          load8(A.post_weight, A.w_f32, i, wp);
+          wp[k].get(wpv);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) g[j] *= rho_y * wp[j];
+          for (int j = 0; j < 8; ++j) g[j] *= rho_y * wpv[j];
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          r[k][j] = __builtin_fmaf(A.scale * g[j], y[k][j], r[k][j]);
-          if (!A.res_f32) r[k][j] = round_bf(r[k][j]);
+          r[k][j] = __builtin_fmaf(A.scale * g[j], y[j], r[k][j]);
+          if (!RF) r[k][j] = round_bf(r[k][j]);
         }
-        store8(A.residual_out, A.res_f32, t * A.H + i, r[k]);
+        store8(A.residual_out, RF, t * A.H + i, r[k]);
       }
     }
     sum[0] = 0.f;
@@ -163,55 +217,88 @@ __global__ void __launch_bounds__(NT == 64 ? 256 : NT) residual_norm_fwd(const N
     for (int k = 0; k < V; ++k) {
       const int64_t i = (int64_t)(tid + k * NT) * 8;
       if (i >= A.H) continue;
-      float w[8], n[8];
-      load8(A.norm_weight, A.w_f32, i, w);
+      float wv[8], n[8];
+      w[k].get(wv);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) n[j] = r[k][j] * rho * w[j];
+      for (int j = 0; j < 8; ++j) n[j] = r[k][j] * rho * wv[j];
       store8(A.normed, false, t * A.H + i, n);
     }
+    R = N;
   }
 }
 
-template <int NT, int V>
+// RF, WF: the residual stream and the weights are float32; CHAN: the gate is per channel.
+template <int NT, int V, bool RF, bool WF, bool CHAN>
 __global__ void __launch_bounds__(NT == 64 ? 256 : NT) residual_norm_bwd(const NormArgs A, const NormGradArgs G) {
   constexpr int RPB = rows_per_block<NT>();
   __shared__ float lds[2 * MAX_THREADS_PER_ROW / 64];
   const int tid = NT == 64 ? (threadIdx.x & 63) : threadIdx.x;
   const int slot = NT == 64 ? threadIdx.x >> 6 : 0;
   const float invH = 1.f / (float)A.H;
-  const bool chan = A.gate_kind == NORM_GATE_CHANNEL;
-  float cw[V][8], cp[V][8], cg[V][8];  // column sums of dw, dwp, dg
+  constexpr bool AHEAD = NT * V <= 1024;  // wider rows have no registers for two of them
+  float cw[V][8], cp[V][8], cg[CHAN ? V : 1][8];  // column sums of dw, dwp, dg
+  Raw8<WF> w[V], wp[V];
 #pragma unroll
-  for (int k = 0; k < V; ++k)
+  for (int k = 0; k < V; ++k) {
+    const int64_t i = (int64_t)(tid + k * NT) * 8;
+    w[k].zero();
+    wp[k].zero();
+    if (i < A.H) {
+      w[k].load(A.norm_weight, i);
+      if (A.post_weight) wp[k].load(A.post_weight, i);
+    }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) cw[k][j] = cp[k][j] = cg[k][j] = 0.f;
-
-  for (int64_t t = (int64_t)blockIdx.x * RPB + slot; t < A.T; t += (int64_t)gridDim.x * RPB) {
-    const float rho = A.rstd[A.T + t];
-    float r[V][8], d[V][8], y[V][8], tr[V][8];
+    for (int j = 0; j < 8; ++j) cw[k][j] = cp[k][j] = cg[CHAN ? k : 0][j] = 0.f;
+  }
+  // a row's data is loaded while the row before it is reduced and written
+  struct Row {
+    Raw8<RF> r[V], tr[V];
+    Raw8<false> d[V], y[V];
+    float rho, rho_y;
+  };
+  auto load = [&](Row& R, int64_t t) {
+    R.rho = A.rstd[A.T + t];
+    R.rho_y = A.y ? A.rstd[t] : 0.f;
 #pragma unroll
     for (int k = 0; k < V; ++k) {
       const int64_t i = (int64_t)(tid + k * NT) * 8;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) r[k][j] = d[k][j] = y[k][j] = tr[k][j] = 0.f;
+      R.r[k].zero();
+      R.tr[k].zero();
+      R.d[k].zero();
+      R.y[k].zero();
       if (i >= A.H) continue;
-      load8(A.residual, A.res_f32, t * A.H + i, r[k]);
-      if (G.d_normed) load8(G.d_normed, false, t * A.H + i, d[k]);
-      if (G.d_residual_out) load8(G.d_residual_out, A.res_f32, t * A.H + i, tr[k]);
-      if (A.y) load8(A.y, false, t * A.H + i, y[k]);
+      R.r[k].load(A.residual, t * A.H + i);
+      if (G.d_normed) R.d[k].load(G.d_normed, t * A.H + i);
+      if (G.d_residual_out) R.tr[k].load(G.d_residual_out, t * A.H + i);
+      if (A.y) R.y[k].load(A.y, t * A.H + i);
     }
+  };
+  const int64_t step = (int64_t)gridDim.x * RPB;
+  int64_t t = (int64_t)blockIdx.x * RPB + slot;
+  Row R;
+  if (AHEAD && t < A.T) load(R, t);
+  for (; t < A.T; t += step) {
+    Row N;
+    if constexpr (AHEAD) {
+      load(N, t + step < A.T ? t + step : t);
+      __builtin_amdgcn_sched_barrier(0);
+    } else {
+      load(R, t);
+    }
+    const float rho = R.rho;
+    float d[V][8], tr[V][8];
     float s1[1] = {0.f};
 #pragma unroll
     for (int k = 0; k < V; ++k) {
-      const int64_t i = (int64_t)(tid + k * NT) * 8;
-      if (i >= A.H) continue;
-      float w[8];
-      load8(A.norm_weight, A.w_f32, i, w);
+      float r[8], wv[8];
+      R.r[k].get(r);
+      R.d[k].get(d[k]);
+      w[k].get(wv);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        cw[k][j] = __builtin_fmaf(d[k][j] * rho, r[k][j], cw[k][j]);
-        d[k][j] *= w[j];
-        s1[0] = __builtin_fmaf(d[k][j], r[k][j], s1[0]);
+        cw[k][j] = __builtin_fmaf(d[k][j] * rho, r[j], cw[k][j]);
+        d[k][j] *= wv[j];
+        s1[0] = __builtin_fmaf(d[k][j], r[j], s1[0]);
       }
     }
     row_sum<NT>(s1, lds);
@@ -219,48 +306,56 @@ __global__ void __launch_bounds__(NT == 64 ? 256 : NT) residual_norm_bwd(const N
 #pragma unroll
     for (int k = 0; k < V; ++k) {
       const int64_t i = (int64_t)(tid + k * NT) * 8;
-      if (i >= A.H) continue;
+      float r[8];
+      R.r[k].get(r);
+      R.tr[k].get(tr[k]);
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        tr[k][j] = __builtin_fmaf(rho, d[k][j], __builtin_fmaf(-c1, r[k][j], tr[k][j]));
-      store8(G.d_residual, A.res_f32, t * A.H + i, tr[k]);
+        tr[k][j] = __builtin_fmaf(rho, d[k][j], __builtin_fmaf(-c1, r[j], tr[k][j]));
+      if (i < A.H) store8(G.d_residual, RF, t * A.H + i, tr[k]);
     }
-    if (!A.y) continue;  // the same for every thread
-    const float rho_y = A.rstd[t];
-    float s2[2] = {0.f, 0.f};  // sum b y, sum s t wp u
+    if (A.y) {  // the same for every thread
+      const float rho_y = R.rho_y;
+      float s2[2] = {0.f, 0.f};  // sum b y, sum s t wp u
 #pragma unroll
-    for (int k = 0; k < V; ++k) {
-      const int64_t i = (int64_t)(tid + k * NT) * 8;
-      if (i >= A.H) continue;
-      float g[8], wp[8], dg[8];
-      gate8(A, t, i, g);
+      for (int k = 0; k < V; ++k) {
+        const int64_t i = (int64_t)(tid + k * NT) * 8;
+        if (i >= A.H) continue;
+        float g[8], wpv[8], dg[8], y[8];
+        gate8(A, t, i, g);
+        R.y[k].get(y);
+        if (A.post_weight)
+          wp[k].get(wpv);
+        else
 #pragma unroll
-      for (int j = 0; j < 8; ++j) wp[j] = 1.f;
-      if (A.post_weight) load8(A.post_weight, A.w_f32, i, wp);
+          for (int j = 0; j < 8; ++j) wpv[j] = 1.f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float st = A.scale * tr[k][j], u = y[k][j] * rho_y;
-        dg[j] = st * wp[j] * u;
-        cg[k][j] += dg[j];
-        s2[1] += dg[j];
-        cp[k][j] = __builtin_fmaf(st * g[j], u, cp[k][j]);
-        tr[k][j] = st * g[j] * wp[j];  // b
-        s2[0] = __builtin_fmaf(tr[k][j], y[k][j], s2[0]);
+        for (int j = 0; j < 8; ++j) {
+          const float st = A.scale * tr[k][j], u = y[j] * rho_y;
+          dg[j] = st * wpv[j] * u;
+          if constexpr (CHAN) cg[k][j] += dg[j];
+          s2[1] += dg[j];
+          cp[k][j] = __builtin_fmaf(st * g[j], u, cp[k][j]);
+          tr[k][j] = st * g[j] * wpv[j];  // b
+          s2[0] = __builtin_fmaf(tr[k][j], y[j], s2[0]);
+        }
+        if (A.gate_kind == NORM_GATE_FULL) store8(G.d_gate, false, t * A.H + i, dg);
       }
-      if (A.gate_kind == NORM_GATE_FULL) store8(G.d_gate, false, t * A.H + i, dg);
-    }
-    row_sum<NT>(s2, lds);
-    if (A.gate_kind == NORM_GATE_TOKEN && tid == 0) static_cast<uint16_t*>(G.d_gate)[t] = f2bf(s2[1]);
-    const float c2 = A.post_weight ? rho_y * rho_y * rho_y * s2[0] * invH : 0.f;
+      row_sum<NT>(s2, lds);
+      if (A.gate_kind == NORM_GATE_TOKEN && tid == 0) static_cast<uint16_t*>(G.d_gate)[t] = f2bf(s2[1]);
+      const float c2 = A.post_weight ? rho_y * rho_y * rho_y * s2[0] * invH : 0.f;
 #pragma unroll
-    for (int k = 0; k < V; ++k) {
-      const int64_t i = (int64_t)(tid + k * NT) * 8;
-      if (i >= A.H) continue;
-      float dy[8];
+      for (int k = 0; k < V; ++k) {
+        const int64_t i = (int64_t)(tid + k * NT) * 8;
+        if (i >= A.H) continue;
+        float dy[8], y[8];
+        R.y[k].get(y);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) dy[j] = __builtin_fmaf(rho_y, tr[k][j], -c2 * y[k][j]);
-      store8(G.d_y, false, t * A.H + i, dy);
+        for (int j = 0; j < 8; ++j) dy[j] = __builtin_fmaf(rho_y, tr[k][j], -c2 * y[j]);
+        store8(G.d_y, false, t * A.H + i, dy);
+      }
     }
+    if constexpr (AHEAD) R = N;
   }
 
   // one partial row per row walker: dw, then dwp, then dg (those that are asked for)
@@ -276,18 +371,19 @@ __global__ void __launch_bounds__(NT == 64 ? 256 : NT) residual_norm_bwd(const N
       store8(p, true, 0, cp[k]);
       p += np * A.H;
     }
-    if (chan) store8(p, true, 0, cg[k]);
+    if constexpr (CHAN) store8(p, true, 0, cg[k]);
   }
 }
 
-// out[c] = sum of the np partial rows of column c, in order: 4 row groups of 64
+// out[c] = sum of the np partial rows of column c, in order: 16 row groups of 64
 // columns each, then the groups.  blockIdx.y names the array.
-__global__ void __launch_bounds__(256) norm_partial_sum(const float* __restrict__ partial, int np, int64_t H,
-                                                        const NormSums S) {
-  __shared__ float part[4][64];
+constexpr int PS_GROUPS = 16;
+__global__ void __launch_bounds__(64 * PS_GROUPS) norm_partial_sum(const float* __restrict__ partial, int np, int64_t H,
+                                                                   const NormSums S) {
+  __shared__ float part[PS_GROUPS][64];
   const int64_t c = (int64_t)blockIdx.x * 64 + (threadIdx.x & 63);
   const int q = threadIdx.x >> 6;
-  const int per = (np + 3) / 4;
+  const int per = (np + PS_GROUPS - 1) / PS_GROUPS;
   const float* p = partial + (int64_t)blockIdx.y * np * H;
   float s = 0.f;
   if (c < H)
@@ -298,7 +394,7 @@ __global__ void __launch_bounds__(256) norm_partial_sum(const float* __restrict_
   if (q || c >= H) return;
   s = 0.f;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) s += part[k][threadIdx.x];
+  for (int k = 0; k < PS_GROUPS; ++k) s += part[k][threadIdx.x];
   void* out = S.out[blockIdx.y];
   if (S.f32[blockIdx.y])
     static_cast<float*>(out)[c] = s;
@@ -317,16 +413,22 @@ hipError_t for_width(int64_t H, F&& f) {
   return f.template operator()<1024, 2>();
 }
 
-constexpr int64_t MAX_FWD_BLOCKS = 1 << 20;
+constexpr int FWD_THREADS = 1 << 19;  // two rounds of resident waves; each row walker takes rows in turn
 struct FwdLaunch {
   const NormArgs& A;
   hipStream_t stream;
+  template <int NT, int V, bool RF, bool WF>
+  void launch() {
+    constexpr int R = rows_per_block<NT>(), B = NT == 64 ? 256 : NT;
+    const int64_t rows = (A.T + R - 1) / R, most = FWD_THREADS / B;
+    residual_norm_fwd<NT, V, RF, WF><<<(unsigned)(rows < most ? rows : most), B, 0, stream>>>(A);
+  }
   template <int NT, int V>
   hipError_t operator()() {
-    constexpr int R = rows_per_block<NT>();
-    const int64_t rows = (A.T + R - 1) / R;
-    // one row per workgroup up to 2^20 workgroups (a launch holds fewer than 2^32 threads)
-    residual_norm_fwd<NT, V><<<(unsigned)(rows < MAX_FWD_BLOCKS ? rows : MAX_FWD_BLOCKS), NT == 64 ? 256 : NT, 0, stream>>>(A);
+    if (A.res_f32)
+      A.w_f32 ? launch<NT, V, true, true>() : launch<NT, V, true, false>();
+    else
+      A.w_f32 ? launch<NT, V, false, true>() : launch<NT, V, false, false>();
     return hipGetLastError();
   }
 };
@@ -337,15 +439,28 @@ struct BwdLaunch {
   hipStream_t stream;
   template <int NT, int V>
   hipError_t operator()() {
-    residual_norm_bwd<NT, V><<<blocks, NT == 64 ? 256 : NT, 0, stream>>>(A, G);
+    if (A.res_f32)
+      A.w_f32 ? launch<NT, V, true, true>() : launch<NT, V, true, false>();
+    else
+      A.w_f32 ? launch<NT, V, false, true>() : launch<NT, V, false, false>();
     return hipGetLastError();
+  }
+  template <int NT, int V, bool RF, bool WF>
+  void launch() {
+    constexpr int B = NT == 64 ? 256 : NT;
+    if (A.gate_kind == NORM_GATE_CHANNEL)
+      residual_norm_bwd<NT, V, RF, WF, true><<<blocks, B, 0, stream>>>(A, G);
+    else
+      residual_norm_bwd<NT, V, RF, WF, false><<<blocks, B, 0, stream>>>(A, G);
   }
 };
 
-constexpr int BWD_ROW_WALKERS = 512;  // workgroups (H > 1024) or waves of the backward
+// Row walkers of the backward, each with one partial row: 1024 waves or 512 workgroups of
+// up to 512 threads (two a CU), 256 of 1024.  8192 rows of 7168: 256 of them 141 us and 5 us
+// for their sums, 512 148 + 14, 1024 159 + 25; 4001 rows of 2048: 512 27 + 8, 256 35 + 5.
 inline int bwd_blocks(int64_t T, int64_t H) {
   const int64_t rpb = H <= 1024 ? 4 : 1;
-  const int64_t b = (T + rpb - 1) / rpb, most = H <= 1024 ? 1024 / 4 : BWD_ROW_WALKERS;
+  const int64_t b = (T + rpb - 1) / rpb, most = H <= 1024 ? 1024 / 4 : H <= 4096 ? 512 : 256;
   return (int)(b < most ? b : most);
 }
 
@@ -375,7 +490,7 @@ hipError_t launch_residual_norm_bwd(const NormArgs& A, const NormGradArgs& G, hi
     S.out[n] = G.d_gate;
     S.f32[n++] = false;
   }
-  norm_partial_sum<<<dim3((unsigned)((A.H + 63) / 64), n), 256, 0, stream>>>(
+  norm_partial_sum<<<dim3((unsigned)((A.H + 63) / 64), n), 64 * PS_GROUPS, 0, stream>>>(
       G.partial, (int)norm_partial_rows(A.T, A.H), A.H, S);
   return hipGetLastError();
 }
