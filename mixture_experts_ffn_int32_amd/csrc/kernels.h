@@ -293,6 +293,7 @@ enum NormGate { NORM_GATE_NONE = 0, NORM_GATE_TOKEN = 1, NORM_GATE_CHANNEL = 2, 
 struct NormArgs {
   int64_t T, H;
   bool res_f32, w_f32;       // types of the residual stream and of the two weights (else bf16)
+  bool stream;               // large bf16 outputs (the launchers set it)
   int gate_kind;
   float eps, scale;
   const uint16_t* y;         // [T][H], or NULL: n = rms(residual) w alone

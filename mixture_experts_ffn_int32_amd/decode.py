@@ -100,9 +100,9 @@ def moe_decode(x, up_proj_weight, down_proj_weight, *, topk_ids=None, topk_weigh
             topk_ids = topk_ids.clamp(-1, E)
         ids, w = ready(topk_ids, torch.int32), ready(topk_weights, torch.float32)
     ud, dd = (ready(up_descale), ready(down_descale)) if fp8 else (None, None)
-    y = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+    y = torch.empty_like(x)
     if T > 0:
-        work = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        work = x.new_empty(nbytes // 2)  # nbytes is a multiple of 256
         with on_device(dev):
             _lib.check(_lib.load().hmm_moe_decode(prob, ptr(x), ptr(wr), ptr(ids), ptr(w), ptr(up_proj_weight), ptr(ud),
                                                   ptr(down_proj_weight), ptr(dd), ptr(y), ptr(work), nbytes, stream_of(dev)))

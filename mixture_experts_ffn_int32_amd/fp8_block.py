@@ -106,7 +106,7 @@ def _linear(x, codes, descale, N):
     dev = x.device
     lib = _lib.load()
     nbytes = _sizes(T, H, N)[0]
-    y = torch.empty((T, N), dtype=torch.bfloat16, device=dev)
+    y = x.new_empty((T, N))
     work = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
     _lib.check(lib.hmm_linear_fp8_block(ptr(x), ptr(codes), ptr(descale), T, H, N, ptr(y), ptr(work), nbytes, stream_of(dev)))
     return y

@@ -65,10 +65,9 @@ def _problem(T, H, residual_dtype, weight_dtype, gate_kind, eps, scale):
 
 def _forward(y, residual, w, wp, g, prob, rstd_wanted):
     """(residual_out, normed, rstd) of arguments that are ready; residual_out None without y."""
-    T, H = residual.shape
-    dev = residual.device
+    T, dev = residual.shape[0], residual.device
     out = None if y is None else torch.empty_like(residual)
-    normed = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+    normed = torch.empty_like(residual, dtype=torch.bfloat16) if y is None else torch.empty_like(y)
     rstd = torch.empty((2, T), dtype=torch.float32, device=dev) if rstd_wanted else None
     if T > 0:
         with on_device(dev):
