@@ -250,14 +250,14 @@ __global__ void __launch_bounds__(RW * 64) block_rows(const uint16_t* __restrict
 // global address, inside one 128-byte line.)
 template <int BM_, int BN_, int WM_, int WN_, int NS_>
 struct BlockTile {
-  static constexpr int SPREAD = 4;
+  static constexpr int SPREAD = 5;  // tiles of a step that its stage loads are spread over
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NS = NS_, NTHR = WM * WN * 64;
   static constexpr int TM = BM / WM, TN = BN / WN, MB = TM / 32, NB = TN / 32;
   static constexpr int STAGE = (BM + BN) * G + BM * 4;  // weight rows, token rows, token scales
   static constexpr int LDO = BN + 8;  // output tile pitch, elements
   static constexpr int LDS = NS * STAGE > BM * LDO * 2 ? NS * STAGE : BM * LDO * 2;
   static_assert(TN <= G && G % TN == 0, "a wave's columns lie in one weight block");
-  static_assert(BM * 8 % NTHR == 0 && BN * 8 % NTHR == 0 && BM % 64 == 0 && NTHR % BM == 0, "whole loads a stage");
+  static_assert(BM * 8 % NTHR == 0 && BN * 8 % NTHR == 0 && BM < NTHR && BM % (NTHR / 64) == 0, "whole loads a stage");
 };
 
 struct BlockArgs {
@@ -286,12 +286,14 @@ __device__ __forceinline__ void load_lds16(u32x4 r, uint32_t lds, uint32_t voff,
                : "s"(lds), "v"(voff), "s"(r), "s"(soff)
                : "memory");
 }
-// the same of 4 bytes per lane
-__device__ __forceinline__ void load_lds4(u32x4 r, uint32_t lds, uint32_t voff, uint32_t soff) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds"
-               :
-               : "s"(lds), "v"(voff), "s"(r), "s"(soff)
-               : "memory");
+// The same of 4 bytes per lane, of the lanes in ``mask`` only; the wave's 64 lanes are active
+// before and after.
+__device__ __forceinline__ void load_lds4(u32x4 r, uint32_t lds, uint32_t voff, uint32_t soff, uint64_t mask) {
+  asm volatile(
+      "s_mov_b32 m0, %0\n\ts_mov_b64 exec, %4\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds\n\ts_mov_b64 exec, -1"
+      :
+      : "s"(lds), "v"(voff), "s"(r), "s"(soff), "s"(mask)
+      : "memory");
 }
 
 __device__ __forceinline__ i32x8 frag(const uint8_t* base, int row, int kk, int half) {
@@ -335,9 +337,10 @@ __global__ void __launch_bounds__(C::NTHR) block_gemm(const BlockArgs A) {
   constexpr int RPL = C::NTHR / 8, LW = C::BN / RPL, LOADS = LW + C::BM / RPL;
   static_assert(RPL % 16 == 0, "permutation period");
   const uint32_t voff = (threadIdx.x >> 3) * pitch + (((threadIdx.x & 7) ^ ((threadIdx.x >> 4) & 7)) * 16);
-  const uint32_t soff = (uint32_t)(threadIdx.x % C::BM) * (uint32_t)groups * 4;
+  constexpr int TPW = C::BM * 64 / C::NTHR;  // tokens whose scales a wave loads
+  const uint32_t soff = (uint32_t)(wave * TPW + lane) * (uint32_t)groups * 4;
   // Loads [from, to) of stage g into its buffer (past the last stage: of the last one again,
-  // unused); the last of them is the scales', 64 tokens a wave.  Rows past the tensors' ends are
+  // unused); the last of them is the scales', BM / waves tokens a wave.  Rows past the tensors' ends are
   // beyond the resources and come back as zeros; the scalar offset stays inside.
   auto stage = [&](int g, int buf, int from, int to) {
     const uint32_t at = lds0 + (uint32_t)buf * C::STAGE;
@@ -348,7 +351,7 @@ __global__ void __launch_bounds__(C::NTHR) block_gemm(const BlockArgs A) {
         load_lds16(i < LW ? rw : rx, at + (uint32_t)(i * C::NTHR + wave * 64) * 16,
                    voff + (uint32_t)(i < LW ? i : i - LW) * RPL * pitch, (uint32_t)gc * G);
       else
-        load_lds4(rs, at + (C::BM + C::BN) * G + (uint32_t)(wave % (C::BM / 64)) * 256, soff, (uint32_t)gc * 4);
+        load_lds4(rs, at + (C::BM + C::BN) * G + (uint32_t)wave * TPW * 4, soff, (uint32_t)gc * 4, (1ull << TPW) - 1);
   };
   constexpr int TILES = C::NB * C::MB, ALL = LOADS + 1, PER = (ALL + (C::SPREAD < TILES ? C::SPREAD : TILES) - 1) / (C::SPREAD < TILES ? C::SPREAD : TILES);
 #pragma unroll
