@@ -1443,6 +1443,19 @@ BlockWork block_work(int64_t rows, int64_t K) {
   w.total = w.xs + up((size_t)rows * (K / 128) * 4);
   return w;
 }
+// the tokens' quantiser, with descales side by side per group, and the product
+hmm_status block_linear(const void* x, const uint8_t* wq, const float* ws, int64_t T, int64_t K, int64_t N, bool ws_transposed,
+                        uint8_t* xq, float* xs, void* y, const char* name, hipStream_t st) {
+  hipError_t e;
+  {
+    Stage stage("quant_rows_block", st);
+    e = hmm::launch_quant_rows_block((const uint16_t*)x, T, K, xq, xs, true, st);
+  }
+  if (e != hipSuccess) return hip_fail(e, "token quantisation launch");
+  Stage stage(name, st);
+  e = hmm::launch_block_gemm(xq, xs, wq, ws, T, K, N, true, ws_transposed, (uint16_t*)y, st);
+  return e == hipSuccess ? HMM_OK : hip_fail(e, "FP8 block product launch");
+}
 size_t block_grad_bytes(int64_t T, int64_t N) { return block_work(T, N).total; }
 }  // namespace
 
@@ -1467,7 +1480,7 @@ hmm_status hmm_quant_rows_block(const void* x, int64_t T, int64_t H, uint8_t* xq
   const bool ne = T > 0;
   if ((s = need(x, ne, "x")) || (s = need(xq, ne, "xq")) || (s = need(xs, ne, "xs"))) return s;
   Stage stage("quant_rows_block", (hipStream_t)stream);
-  const hipError_t e = hmm::launch_quant_rows_block((const uint16_t*)x, T, H, xq, xs, (hipStream_t)stream);
+  const hipError_t e = hmm::launch_quant_rows_block((const uint16_t*)x, T, H, xq, xs, false, (hipStream_t)stream);
   return e == hipSuccess ? HMM_OK : hip_fail(e, "token quantisation launch");
 }
 
@@ -1481,7 +1494,7 @@ hmm_status hmm_matmul_fp8_block(const uint8_t* xq, const float* xs, const uint8_
     return s;
   if (!ne) return HMM_OK;
   Stage stage("matmul_fp8_block", (hipStream_t)stream);
-  const hipError_t e = hmm::launch_block_gemm(xq, xs, codes_t, descale, T, H, N, false, (uint16_t*)y, (hipStream_t)stream);
+  const hipError_t e = hmm::launch_block_gemm(xq, xs, codes_t, descale, T, H, N, false, false, (uint16_t*)y, (hipStream_t)stream);
   return e == hipSuccess ? HMM_OK : hip_fail(e, "FP8 block product launch");
 }
 
@@ -1514,8 +1527,7 @@ hmm_status hmm_linear_fp8_block(const void* x, const uint8_t* codes_t, const flo
     return fail(HMM_ERR_WORKSPACE_TOO_SMALL, "workspace is %zu bytes, %zu needed", workspace_bytes, w.total);
   uint8_t* xq = at<uint8_t>(workspace, w.xq);
   float* xs = at<float>(workspace, w.xs);
-  if ((s = hmm_quant_rows_block(x, T, H, xq, xs, stream)) != HMM_OK) return s;
-  return hmm_matmul_fp8_block(xq, xs, codes_t, descale, T, H, N, y, stream);
+  return block_linear(x, codes_t, descale, T, H, N, false, xq, xs, y, "matmul_fp8_block", st);
 }
 
 hmm_status hmm_linear_fp8_block_grad(const void* dy, const void* x, const uint8_t* codes, const float* descale, int64_t T,
@@ -1538,10 +1550,7 @@ hmm_status hmm_linear_fp8_block_grad(const void* dy, const void* x, const uint8_
   if (ne && dx) {
     uint8_t* gq = at<uint8_t>(workspace, w.xq);
     float* gs = at<float>(workspace, w.xs);
-    if ((s = hmm_quant_rows_block(dy, T, N, gq, gs, stream)) != HMM_OK) return s;
-    Stage stage("matmul_fp8_block_dx", st);
-    const hipError_t e = hmm::launch_block_gemm(gq, gs, codes, descale, T, N, H, true, (uint16_t*)dx, st);
-    if (e != hipSuccess) return hip_fail(e, "FP8 block product launch");
+    if ((s = block_linear(dy, codes, descale, T, N, H, true, gq, gs, dx, "matmul_fp8_block_dx", st)) != HMM_OK) return s;
   }
   if (dw) {
     Stage stage("linear_fp8_block_dw", st);

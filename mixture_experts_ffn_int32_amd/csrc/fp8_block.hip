@@ -98,8 +98,11 @@ __global__ void __launch_bounds__(QB_THREADS) quant_block(const uint16_t* __rest
 constexpr int QR_THREADS = 256;
 constexpr int64_t QR_MAX_BLOCKS = 1 << 20;
 
-__global__ void __launch_bounds__(QR_THREADS) quant_rows_block(const uint16_t* __restrict__ x, int64_t chunks,
-                                                               uint8_t* __restrict__ xq, float* __restrict__ xs) {
+// COLS: the descales as [H / 128][T], so that the product reads those of a group side by side.
+// (T H / 128 stays below 2^32: the codes alone would not fit the card otherwise.)
+template <bool COLS>
+__global__ void __launch_bounds__(QR_THREADS) quant_rows_block(const uint16_t* __restrict__ x, int64_t chunks, uint32_t groups,
+                                                               uint32_t T, uint8_t* __restrict__ xq, float* __restrict__ xs) {
   for (int64_t c = (int64_t)blockIdx.x * QR_THREADS + threadIdx.x; c < chunks; c += (int64_t)gridDim.x * QR_THREADS) {
     float v[8], s[8];
     unpack8(*reinterpret_cast<const u32x4*>(x + c * 8), v);
@@ -112,7 +115,8 @@ __global__ void __launch_bounds__(QR_THREADS) quant_rows_block(const uint16_t* _
 #pragma unroll
     for (int j = 0; j < 8; ++j) s[j] = sc;
     *reinterpret_cast<uint2*>(xq + c * 8) = to_e4m3x8(v, s);
-    if ((c & 15) == 0) xs[c >> 4] = 1.f / sc;
+    const uint32_t i = (uint32_t)(c >> 4);
+    if ((c & 15) == 0) xs[COLS ? (int64_t)(i % groups) * T + i / groups : (int64_t)i] = 1.f / sc;
   }
 }
 
@@ -265,6 +269,7 @@ struct BlockArgs {
   const float *xs, *ws;
   int64_t T, H, N;
   int ws_n, ws_g;  // steps of ws from one column block and from one group to the next
+  int64_t xs_t, xs_g;  // and of xs from one token and from one group to the next
   uint16_t* y;
   int mt, nt;
 };
@@ -320,7 +325,7 @@ __global__ void __launch_bounds__(C::NTHR) block_gemm(const BlockArgs A) {
   const u32x4 rx = rsrc_words(A.xq + m0 * A.H, min((int64_t)C::BM, A.T - m0) * A.H);
   const u32x4 rw = rsrc_words(A.wq + n0 * A.H, min((int64_t)C::BN, A.N - n0) * A.H);
   const int groups = (int)(A.H / G);
-  const u32x4 rs = rsrc_words(A.xs + m0 * groups, min((int64_t)C::BM, A.T - m0) * groups * 4);
+  const u32x4 rs = rsrc_words(A.xs + m0 * A.xs_t, (A.T * groups - m0 * A.xs_t) * 4);
   const float* wsp = A.ws + ((n0 + wn * C::TN) / G < (A.N + G - 1) / G ? (n0 + wn * C::TN) / G : 0) * A.ws_n;
 
   f32x16 acc[C::NB][C::MB];
@@ -338,7 +343,7 @@ __global__ void __launch_bounds__(C::NTHR) block_gemm(const BlockArgs A) {
   static_assert(RPL % 16 == 0, "permutation period");
   const uint32_t voff = (threadIdx.x >> 3) * pitch + (((threadIdx.x & 7) ^ ((threadIdx.x >> 4) & 7)) * 16);
   constexpr int TPW = C::BM * 64 / C::NTHR;  // tokens whose scales a wave loads
-  const uint32_t soff = (uint32_t)(wave * TPW + lane) * (uint32_t)groups * 4;
+  const uint32_t soff = (uint32_t)min((int64_t)(wave * TPW + lane), A.T - 1 - m0) * (uint32_t)A.xs_t * 4;
   // Loads [from, to) of stage g into its buffer (past the last stage: of the last one again,
   // unused); the last of them is the scales', BM / waves tokens a wave.  Rows past the tensors' ends are
   // beyond the resources and come back as zeros; the scalar offset stays inside.
@@ -351,7 +356,7 @@ __global__ void __launch_bounds__(C::NTHR) block_gemm(const BlockArgs A) {
         load_lds16(i < LW ? rw : rx, at + (uint32_t)(i * C::NTHR + wave * 64) * 16,
                    voff + (uint32_t)(i < LW ? i : i - LW) * RPL * pitch, (uint32_t)gc * G);
       else
-        load_lds4(rs, at + (C::BM + C::BN) * G + (uint32_t)wave * TPW * 4, soff, (uint32_t)gc * 4, (1ull << TPW) - 1);
+        load_lds4(rs, at + (C::BM + C::BN) * G + (uint32_t)wave * TPW * 4, soff, (uint32_t)(gc * A.xs_g) * 4, (1ull << TPW) - 1);
   };
   constexpr int TILES = C::NB * C::MB, ALL = LOADS + 1, PER = (ALL + (C::SPREAD < TILES ? C::SPREAD : TILES) - 1) / (C::SPREAD < TILES ? C::SPREAD : TILES);
 #pragma unroll
@@ -459,10 +464,15 @@ hipError_t launch_quant_block(const uint16_t* w, int64_t E, int64_t H, int64_t N
   return hipGetLastError();
 }
 
-hipError_t launch_quant_rows_block(const uint16_t* x, int64_t T, int64_t H, uint8_t* xq, float* xs, hipStream_t stream) {
+hipError_t launch_quant_rows_block(const uint16_t* x, int64_t T, int64_t H, uint8_t* xq, float* xs, bool cols,
+                                   hipStream_t stream) {
   const int64_t chunks = T * (H / 8), blocks = (chunks + QR_THREADS - 1) / QR_THREADS;
   if (chunks <= 0) return hipSuccess;
-  quant_rows_block<<<(unsigned)(blocks < QR_MAX_BLOCKS ? blocks : QR_MAX_BLOCKS), QR_THREADS, 0, stream>>>(x, chunks, xq, xs);
+  const unsigned grid = (unsigned)(blocks < QR_MAX_BLOCKS ? blocks : QR_MAX_BLOCKS);
+  if (cols)
+    quant_rows_block<true><<<grid, QR_THREADS, 0, stream>>>(x, chunks, (uint32_t)(H / G), (uint32_t)T, xq, xs);
+  else
+    quant_rows_block<false><<<grid, QR_THREADS, 0, stream>>>(x, chunks, (uint32_t)(H / G), (uint32_t)T, xq, xs);
   return hipGetLastError();
 }
 
@@ -474,9 +484,10 @@ hipError_t launch_block_rows(const uint16_t* x, const uint8_t* wq, const float* 
 }
 
 hipError_t launch_block_gemm(const uint8_t* xq, const float* xs, const uint8_t* wq, const float* ws, int64_t T, int64_t H,
-                             int64_t N, bool ws_transposed, uint16_t* y, hipStream_t stream) {
+                             int64_t N, bool xs_cols, bool ws_transposed, uint16_t* y, hipStream_t stream) {
   const int groups = (int)(H / G), nbs = (int)((N + G - 1) / G);
-  const BlockArgs a{xq, wq, xs, ws, T, H, N, ws_transposed ? 1 : groups, ws_transposed ? nbs : 1, y, 0, 0};
+  const BlockArgs a{xq, wq, xs, ws, T, H, N, ws_transposed ? 1 : groups, ws_transposed ? nbs : 1, xs_cols ? 1 : groups,
+                    xs_cols ? T : 1, y, 0, 0};
   const auto tiles = [&](int64_t bm, int64_t bn) { return ((T + bm - 1) / bm) * ((N + bn - 1) / bn); };
   if (tiles(256, 256) >= 192) return launch_gemm<BlockTile<256, 256, 4, 2, 2>>(a, stream);
   if (tiles(128, 128) >= 192) return launch_gemm<BlockTile<128, 128, 2, 2, 2>>(a, stream);

@@ -349,14 +349,15 @@ hipError_t launch_moe_decode(const DecodeArgs& A, bool fp8, hipStream_t stream);
 //   w [E][H][N] bf16 -> qt [E][N][H] and / or q [E][H][N] (NULL: not written), ds [E][ceil(N/128)][H/128]
 hipError_t launch_quant_block(const uint16_t* w, int64_t E, int64_t H, int64_t N, uint8_t* qt, uint8_t* q, float* ds,
                               hipStream_t stream);
-//   x [T][H] bf16 -> xq [T][H] E4M3, xs [T][H/128]
-hipError_t launch_quant_rows_block(const uint16_t* x, int64_t T, int64_t H, uint8_t* xq, float* xs, hipStream_t stream);
+//   x [T][H] bf16 -> xq [T][H] E4M3, xs [T][H/128], or [H/128][T] with cols
+hipError_t launch_quant_rows_block(const uint16_t* x, int64_t T, int64_t H, uint8_t* xq, float* xs, bool cols,
+                                   hipStream_t stream);
 constexpr int BLOCK_MAX_ROWS = 64;  // tokens up to which launch_block_rows takes them
 //   y [T][N] of bf16 tokens x [T][H], quantised on the way (T <= BLOCK_MAX_ROWS)
 hipError_t launch_block_rows(const uint16_t* x, const uint8_t* wq, const float* ws, int T, int64_t H, int64_t N, uint16_t* y,
                              hipStream_t stream);
-//   y [T][N] of codes xq [T][H], xs [T][H/128]; ws [ceil(N/128)][H/128], or its transpose
+//   y [T][N] of codes xq [T][H], xs as the quantiser wrote them; ws [ceil(N/128)][H/128], or its transpose
 hipError_t launch_block_gemm(const uint8_t* xq, const float* xs, const uint8_t* wq, const float* ws, int64_t T, int64_t H,
-                             int64_t N, bool ws_transposed, uint16_t* y, hipStream_t stream);
+                             int64_t N, bool xs_cols, bool ws_transposed, uint16_t* y, hipStream_t stream);
 
 }  // namespace hmm
