@@ -487,7 +487,8 @@ hmm_status hmm_moe_decode(const hmm_decode_problem* p, const void* x, const void
  *   (the quantisation of x and of the weight is passed through: their derivative is
  *   taken as 1).  T = 0 writes dw = 0.
  * T >= 0; H a multiple of 128 in [128, 65536]; N a multiple of 16 in [16, 262144], in the
- * gradient of 128.  dw needs x and dy below 4 GiB each (else HMM_ERR_UNSUPPORTED). */
+ * gradient of 128.  dw needs x and dy below 4 GiB each, and every call T max(H, N) / 128
+ * descales below 4 GiB (else HMM_ERR_UNSUPPORTED). */
 hmm_status hmm_quant_block(const void* w, int64_t E, int64_t H, int64_t N, uint8_t* codes_t, uint8_t* codes, float* descale,
                            void* stream);
 hmm_status hmm_quant_rows_block(const void* x, int64_t T, int64_t H, uint8_t* xq, float* xs, void* stream);

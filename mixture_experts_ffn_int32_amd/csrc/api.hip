@@ -1431,6 +1431,9 @@ hmm_status block_dims(int64_t T, int64_t H, int64_t N, int64_t nstep) {
   if (H < 128 || H % 128 || H > 65536) return fail(HMM_ERR_BAD_SHAPE, "H must be a multiple of 128 in [128, 65536] (got %lld)", (long long)H);
   if (N < nstep || N % nstep || N > 65536 * 4)
     return fail(HMM_ERR_BAD_SHAPE, "N must be a multiple of %lld in [%lld, 262144] (got %lld)", (long long)nstep, (long long)nstep, (long long)N);
+  // the descales of a token or gradient row are addressed through one 4 GiB buffer
+  const int64_t groups = (H > N ? H : N) / 128;
+  if (T * groups >= (int64_t)1 << 30) return fail(HMM_ERR_UNSUPPORTED, "T is %lld: the descales must be below 4 GiB", (long long)T);
   return HMM_OK;
 }
 struct BlockWork {

@@ -220,6 +220,7 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 // after a transposition in registers (one v_perm_b32 per pair) is its operand for each of
 // the 8 columns of the chunk.  Sub-tile c holds the columns 8 m + c of chunk m.
 struct Bf16Weights {
+  static constexpr bool WIDE = true;
   static constexpr int SUB = 8, COLS = 128, DEPTH = 32, LOADS = 8;
   static constexpr int ROW_LOADS = 1;  // 16-byte loads of a row (token) per step
   static __device__ __forceinline__ int column(int c, int m) { return 8 * m + c; }
@@ -267,6 +268,7 @@ struct Bf16Weights {
 // descale in float32.
 template <int D>
 struct Fp8Weights {
+  static constexpr bool WIDE = false;
   static constexpr int SUB = 4, COLS = 64, DEPTH = D, CL = D / 64, LOADS = 4 * CL;  // CL: loads per column
   static constexpr int ROW_LOADS = 2 * CL;
   static __device__ __forceinline__ int column(int c, int m) { return 16 * c + m; }
@@ -686,38 +688,36 @@ void launch_down(const DecodeArgs& A, int64_t act, hipStream_t stream) {
 
 constexpr int SUM_TOKENS = 4;
 
-// WA: weights of up to 16 tokens (one row tile), WB: of more
+// WA: weights of up to 16 tokens (one row tile), WB: of more.  Wide tiles (a wave's 128 columns
+// side by side) where they still give every workgroup a unit: up-projection of 32 experts, H =
+// 7168, I = 2048, 64 tokens 332 us wide, 371 narrow; 86 chosen experts, H = 2048, I = 768, 17
+// tokens 91 / 95; down-projection of the latter 56 / 61, of the former 200 / 198.  With E4M3
+// weights wide tiles gained nothing (93 / 89).
 template <class WA, class WB, int DW>
 hipError_t launch_experts(const DecodeArgs& A, hipStream_t stream) {
   const int64_t act = A.E < A.T * A.K ? A.E : A.T * A.K;  // experts that may be chosen
-  const bool wide = A.wbytes == 2 && A.I % 128 == 0 && act * (A.I / 128) >= MAX_GROUPS;
-  if (A.T <= 16) {
-    if (wide)
-      launch_up<WA, 1, DW, true>(A, act, stream);
-    else
-      launch_up<WA, 1, DW, false>(A, act, stream);
-  } else {
-    if (wide)
-      launch_up<WB, 2, DW, true>(A, act, stream);
-    else
-      launch_up<WB, 2, DW, false>(A, act, stream);
+  const bool few = A.T <= 16;
+  bool up = false, down = false;
+  if constexpr (WA::WIDE) {
+    if (A.I % WA::COLS == 0 && act * (A.I / WA::COLS) >= MAX_GROUPS) {
+      few ? launch_up<WA, 1, DW, true>(A, act, stream) : launch_up<WB, 2, DW, true>(A, act, stream);
+      up = true;
+    }
   }
+  if (!up) few ? launch_up<WA, 1, DW, false>(A, act, stream) : launch_up<WB, 2, DW, false>(A, act, stream);
+  // Up to 4 tokens the down-projection adds the rows up itself (1 token, 32 experts: 47.5 us, 42.9
+  // and 4.8 with the sum as a launch of its own; 64 tokens 244 us, 197 and 6).
   if (A.T <= SUM_TOKENS) {
     launch_down<WA, 1, DW, 1, true>(A, act, stream);
     return hipGetLastError();
   }
-  const bool wider = A.wbytes == 2 && act * (A.H / (2 * WA::COLS)) >= MAX_GROUPS;
-  if (A.T <= 16) {
-    if (wider)
-      launch_down<WA, 1, DW, 2, false>(A, act, stream);
-    else
-      launch_down<WA, 1, DW, 1, false>(A, act, stream);
-  } else {
-    if (wider)
-      launch_down<WB, 2, DW, 2, false>(A, act, stream);
-    else
-      launch_down<WB, 2, DW, 1, false>(A, act, stream);
+  if constexpr (WA::WIDE) {
+    if (act * (A.H / (2 * WA::COLS)) >= MAX_GROUPS) {
+      few ? launch_down<WA, 1, DW, 2, false>(A, act, stream) : launch_down<WB, 2, DW, 2, false>(A, act, stream);
+      down = true;
+    }
   }
+  if (!down) few ? launch_down<WA, 1, DW, 1, false>(A, act, stream) : launch_down<WB, 2, DW, 1, false>(A, act, stream);
   decode_combine<<<dim3((unsigned)((A.H / 4 + CT - 1) / CT), A.T), CT, 0, stream>>>(A);
   return hipGetLastError();
 }

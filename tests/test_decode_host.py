@@ -56,11 +56,12 @@ def test_decode_pointers(lib):
 @pytest.mark.parametrize("T,H,N,status", [
     (-1, 128, 128, _lib.HMM_ERR_BAD_SHAPE), (1 << 31, 128, 128, _lib.HMM_ERR_BAD_SHAPE), (4, 64, 128, _lib.HMM_ERR_BAD_SHAPE),
     (4, 192, 128, _lib.HMM_ERR_BAD_SHAPE), (4, 65664, 128, _lib.HMM_ERR_BAD_SHAPE), (4, 128, 8, _lib.HMM_ERR_BAD_SHAPE),
-    (4, 128, 0, _lib.HMM_ERR_BAD_SHAPE), (4, 128, 262160, _lib.HMM_ERR_BAD_SHAPE), (4, 128, 16, _lib.HMM_OK), (0, 128, 16, _lib.HMM_OK)])
+    (4, 128, 0, _lib.HMM_ERR_BAD_SHAPE), (4, 128, 262160, _lib.HMM_ERR_BAD_SHAPE), (1 << 30, 128, 128, _lib.HMM_ERR_UNSUPPORTED),
+    (4, 128, 16, _lib.HMM_OK), (0, 128, 16, _lib.HMM_OK)])
 def test_block_dims(lib, T, H, N, status):
     a, b = ctypes.c_size_t(), ctypes.c_size_t()
     assert lib.hmm_linear_fp8_block_sizes(T, H, N, ctypes.byref(a), ctypes.byref(b)) == status
-    assert lib.hmm_matmul_fp8_block(Z, Z, OK, OK, T, H, N, Z, Z) == (status or (_lib.HMM_ERR_NULL_POINTER if T else 0))
+    assert lib.hmm_matmul_fp8_block(Z, Z, OK, OK, T, H, N, Z, Z) == (status or (_lib.HMM_ERR_NULL_POINTER if T else 0))  # no data pointers: a valid shape is refused for them
 
 
 def test_block_pointers(lib):

@@ -64,6 +64,8 @@ SHAPES = [  # T, H, I, E, K, fp8
     (1, 64, 64, 1, 1, False), (1, 512, 128, 4, 2, False), (4, 512, 128, 4, 2, False), (3, 192, 320, 5, 3, False),
     (16, 256, 192, 33, 8, False), (17, 448, 64, 7, 2, False), (32, 320, 128, 3, 3, False), (33, 128, 192, 6, 1, False),
     (64, 256, 128, 4, 4, False), (64, 576, 64, 70, 8, False), (2, 128, 64, 1024, 16, False),
+    # wide tiles of both projections, with a last column tile of 64, for one and for two row tiles
+    (16, 1088, 512, 128, 8, False), (64, 1088, 512, 128, 8, False),
     (1, 128, 128, 1, 1, True), (5, 512, 128, 4, 2, True), (16, 256, 384, 9, 4, True), (23, 640, 128, 5, 3, True),
     (64, 384, 256, 6, 6, True), (48, 256, 128, 40, 2, True),
 ]
