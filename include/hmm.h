@@ -479,7 +479,7 @@ hmm_status hmm_moe_decode(const hmm_decode_problem* p, const void* x, const void
  *   bytes (NULL: not written; one at least), descale [E,ceil(N/128),H/128] float32.
  * hmm_matmul_fp8_block: the product of codes.
  * hmm_linear_fp8_block: x bf16 [T,H] quantised as hmm_quant_rows_block does, then
- *   the product; for T <= 64 in one launch without workspace (forward_bytes is 0 then).
+ *   the product; for T <= 16 in one launch without workspace (forward_bytes is 0 then).
  * hmm_linear_fp8_block_grad: of dy bf16 [T,N],
  *   dx bf16 [T,H]: dy quantised per token and 128 of N, times the same codes (in the
  *                  layout ``codes`` [H,N]) and descales, along N; NULL: not computed

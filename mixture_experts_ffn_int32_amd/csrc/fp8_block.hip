@@ -121,129 +121,168 @@ __global__ void __launch_bounds__(QR_THREADS) quant_rows_block(const uint16_t* _
 }
 
 // ------------------------------------------------------------------- few rows
-// T <= 64: bound by the weight's bytes.  A workgroup owns 16 SUB columns; its 8 waves
-// take the groups in turn, streaming codes from global memory into registers.  The
-// tokens are read in bf16 and quantised in registers (a group of a token is held by the
-// four lanes that share it), which gives exactly the codes of the row quantiser.  Codes
-// of both operands become bf16 (exact) for the 16x16x32 instruction, whose products are
-// exact and whose sums are float32.
-constexpr int RW = 8;
+// Bound by the weight's bytes.  A workgroup owns 16 columns; its RW waves take the groups in
+// turn, streaming codes from global memory into two register sets, and add their sums up in LDS
+// at the end.  Lane l holds 32 codes of a group, k = 32 (l / 16) + 0.., of weight row and of
+// token l % 16.
+struct BlockArgs {
+  const uint8_t *xq, *wq;
+  const float *xs, *ws;
+  int64_t T, H, N;
+  int ws_n, ws_g;      // steps of ws from one column block and from one group to the next
+  int64_t xs_t, xs_g;  // and of xs from one token and from one group to the next
+  uint16_t* y;
+  int mt, nt;          // tiles of the many-row kernel
+};
 
-template <int SUB, int NT>
+// y of 16 columns and the tokens 16 n + 0..15 from the waves' sums
+template <int RW>
+__device__ __forceinline__ void put_rows(float (&part)[RW][16][20], f32x4 acc, int n, int64_t T, int64_t N, int64_t n0,
+                                         uint16_t* y) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  *reinterpret_cast<f32x4*>(&part[wave][lane & 15][4 * (lane >> 4)]) = acc;
+  __syncthreads();
+  const int t = threadIdx.x >> 4, col = threadIdx.x & 15;
+  if (threadIdx.x < 256 && n * 16 + t < T && n0 + col < N) {
+    float s = 0.f;
+#pragma unroll
+    for (int q = 0; q < RW; ++q) s += part[q][t][col];
+    y[(int64_t)(n * 16 + t) * N + n0 + col] = f2bf(s);
+  }
+  __syncthreads();
+}
+
+// Up to 16 bf16 tokens, quantised in registers (a group of a token is held by the four lanes that
+// share it), which gives exactly the codes of the token quantiser in one launch.  Codes of both
+// operands become bf16 (exact) for the 16x16x32 instruction: products are exact, sums float32.
+template <int RW>
 __global__ void __launch_bounds__(RW * 64) block_rows(const uint16_t* __restrict__ x, const uint8_t* __restrict__ wq,
                                                       const float* __restrict__ ws, int T, int64_t H, int64_t N,
                                                       uint16_t* __restrict__ y) {
-  constexpr int COLS = 16 * SUB, LD = COLS + 4;
-  __shared__ float part[RW][16][LD];
+  __shared__ float part[RW][16][20];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int row = lane & 15, quad = lane >> 4;
-  const int64_t n0 = (int64_t)blockIdx.x * COLS;
+  const int64_t n0 = (int64_t)blockIdx.x * 16;
   const int groups = (int)(H / G);
-  const uint8_t* wp[SUB];
-#pragma unroll
-  for (int c = 0; c < SUB; ++c) wp[c] = wq + min(n0 + 16 * c + row, N - 1) * H + 32 * quad;
-  const uint16_t* xp[NT];
-#pragma unroll
-  for (int n = 0; n < NT; ++n) xp[n] = x + (int64_t)min(n * 16 + row, T - 1) * H + 32 * quad;
+  const uint8_t* wp = wq + min(n0 + row, N - 1) * H + 32 * quad;
+  const uint16_t* xp = x + (int64_t)min(row, T - 1) * H + 32 * quad;
   const float* wsp = ws + (n0 / G) * groups;
-  f32x4 acc[SUB][NT];
+  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+  u32x4 w[2][2], b[2][4];
+  auto load = [&](int g, u32x4 (&wr)[2], u32x4 (&br)[4]) {
+    if (g >= groups) return;
 #pragma unroll
-  for (int c = 0; c < SUB; ++c)
+    for (int i = 0; i < 2; ++i) wr[i] = *reinterpret_cast<const u32x4*>(wp + (int64_t)g * G + 16 * i);
 #pragma unroll
-    for (int n = 0; n < NT; ++n) acc[c][n] = f32x4{0.f, 0.f, 0.f, 0.f};
-
-  u32x4 w[SUB][2], b[NT][4];
-  auto load = [&](int g, u32x4 (&wr)[SUB][2], u32x4 (&br)[NT][4]) {
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) br[n][q] = *reinterpret_cast<const u32x4*>(xp[n] + (int64_t)g * G + 8 * q);
-#pragma unroll
-    for (int c = 0; c < SUB; ++c)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) wr[c][i] = *reinterpret_cast<const u32x4*>(wp[c] + (int64_t)g * G + 16 * i);
+    for (int q = 0; q < 4; ++q) br[q] = *reinterpret_cast<const u32x4*>(xp + (int64_t)g * G + 8 * q);
+    __builtin_amdgcn_sched_barrier(0);  // the loads go out here, not where their data is needed
   };
-  if (wave < groups) load(wave, w, b);
-  for (int g = wave; g < groups; g += RW) {
-    u32x4 wn[SUB][2], bn[NT][4];
-    if (g + RW < groups) load(g + RW, wn, bn);
-    const float sw = wsp[g];
-    // tokens: maximum of the group over this lane's 32 elements and the other three quads
-    float sx[NT];
+  auto bf16_of = [](uint32_t v, bool high) {
+    return __builtin_bit_cast(uint32_t, high ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v, 1.0f, true)
+                                             : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v, 1.0f, false));
+  };
+  auto group = [&](int g, const u32x4 (&w)[2], const u32x4 (&b)[4]) {
+    if (g >= groups) return;
+    float v[4][8], m = 0.f;
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      float m = 0.f;
-      float v[4][8];
+    for (int q = 0; q < 4; ++q) {
+      unpack8(b[q], v[q]);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        unpack8(b[n][q], v[q]);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(v[q][j]));
-      }
-      m = fmaxf(m, __shfl_xor(m, 16));
-      m = fmaxf(m, __shfl_xor(m, 32));
-      const float sc = block_scale_of(m);
-      sx[n] = sw * (1.f / sc);
-      float s[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) s[j] = sc;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const uint2 code = to_e4m3x8(v[q], s);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          b[n][q][i] = __builtin_bit_cast(
-              uint32_t, i & 1 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(i < 2 ? code.x : code.y, 1.0f, true)
-                              : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(i < 2 ? code.x : code.y, 1.0f, false));
-      }
+      for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(v[q][j]));
     }
+    m = fmaxf(m, __shfl_xor(m, 16));
+    m = fmaxf(m, __shfl_xor(m, 32));
+    const float sc = block_scale_of(m);
+    const float s[8] = {sc, sc, sc, sc, sc, sc, sc, sc};
+    f32x4 t = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int c = 0; c < SUB; ++c) {
-      u32x4 a[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint32_t v = w[c][q >> 1][2 * (q & 1) + i];
-          a[q][2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v, 1.0f, false));
-          a[q][2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v, 1.0f, true));
-        }
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        f32x4 t = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a[q]), __builtin_bit_cast(bf16x8, b[n][q]),
-                                                      t, 0, 0, 0);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[c][n][i] = __builtin_fmaf(sx[n], t[i], acc[c][n][i]);
-      }
+    for (int q = 0; q < 4; ++q) {
+      const uint2 code = to_e4m3x8(v[q], s);
+      const uint32_t w0 = w[q >> 1][2 * (q & 1)], w1 = w[q >> 1][2 * (q & 1) + 1];
+      const u32x4 a = {bf16_of(w0, false), bf16_of(w0, true), bf16_of(w1, false), bf16_of(w1, true)};
+      const u32x4 c = {bf16_of(code.x, false), bf16_of(code.x, true), bf16_of(code.y, false), bf16_of(code.y, true)};
+      t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, c), t, 0, 0, 0);
     }
+    const float sx = wsp[g] * (1.f / sc);
 #pragma unroll
-    for (int c = 0; c < SUB; ++c)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) w[c][i] = wn[c][i];
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) b[n][q] = bn[n][q];
+    for (int i = 0; i < 4; ++i) acc[i] = __builtin_fmaf(sx, t[i], acc[i]);
+  };
+  load(wave, w[0], b[0]);
+  load(wave + RW, w[1], b[1]);
+  for (int g = wave; g < groups; g += 2 * RW) {
+    group(g, w[0], b[0]);
+    load(g + 2 * RW, w[0], b[0]);
+    group(g + RW, w[1], b[1]);
+    load(g + 3 * RW, w[1], b[1]);
   }
+  put_rows<RW>(part, acc, 0, T, N, n0, y);
+}
+
+// Up to 16 NT tokens' codes: one 16x16x128 instruction a group and row tile.
+template <int NT, int RW>
+__global__ void __launch_bounds__(RW * 64) block_codes(const BlockArgs A) {
+  __shared__ float part[RW][16][20];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int row = lane & 15, quad = lane >> 4;
+  const int64_t n0 = (int64_t)blockIdx.x * 16;
+  const int groups = (int)(A.H / G);
+  const uint8_t* wp = A.wq + min(n0 + row, A.N - 1) * A.H + 32 * quad;
+  const uint8_t* xp[NT];
+  const float* sp[NT];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    if (n) __syncthreads();
-#pragma unroll
-    for (int c = 0; c < SUB; ++c) *reinterpret_cast<f32x4*>(&part[wave][row][16 * c + 4 * quad]) = acc[c][n];
-    __syncthreads();
-    for (int i = threadIdx.x; i < 16 * COLS; i += RW * 64) {
-      const int t = n * 16 + i / COLS, col = i % COLS;
-      if (t >= T || n0 + col >= N) continue;
-      float s = 0.f;
-#pragma unroll
-      for (int q = 0; q < RW; ++q) s += part[q][i / COLS][col];
-      y[(int64_t)t * N + n0 + col] = f2bf(s);
-    }
+    const int64_t t = min((int64_t)(n * 16 + row), A.T - 1);
+    xp[n] = A.xq + t * A.H + 32 * quad;
+    sp[n] = A.xs + t * A.xs_t;
   }
+  const float* wsp = A.ws + (n0 / G) * A.ws_n;
+  f32x4 acc[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) acc[n] = f32x4{0.f, 0.f, 0.f, 0.f};
+  struct Set {
+    u32x4 w[2], b[NT][2];
+    float s[NT];
+  } set[2];
+  auto load = [&](int g, Set& S) {
+    if (g >= groups) return;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) S.w[i] = *reinterpret_cast<const u32x4*>(wp + (int64_t)g * G + 16 * i);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) S.b[n][i] = *reinterpret_cast<const u32x4*>(xp[n] + (int64_t)g * G + 16 * i);
+      S.s[n] = sp[n][g * A.xs_g];
+    }
+    __builtin_amdgcn_sched_barrier(0);  // the loads go out here, not where their data is needed
+  };
+  auto join = [](const u32x4 (&v)[2]) {
+    return i32x8{(int)v[0][0], (int)v[0][1], (int)v[0][2], (int)v[0][3], (int)v[1][0], (int)v[1][1], (int)v[1][2], (int)v[1][3]};
+  };
+  auto group = [&](int g, const Set& S) {
+    if (g >= groups) return;
+    const float sw = wsp[(int64_t)g * A.ws_g];
+    const i32x8 a = join(S.w);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+      const f32x4 t = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, join(S.b[n]), zero, 0, 0, 0, 127, 0, 127);
+      const float s = S.s[n] * sw;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[n][i] = __builtin_fmaf(s, t[i], acc[n][i]);
+    }
+  };
+  load(wave, set[0]);
+  load(wave + RW, set[1]);
+  for (int g = wave; g < groups; g += 2 * RW) {
+    group(g, set[0]);
+    load(g + 2 * RW, set[0]);
+    group(g + RW, set[1]);
+    load(g + 3 * RW, set[1]);
+  }
+#pragma unroll
+  for (int n = 0; n < NT; ++n) put_rows<RW>(part, acc[n], n, A.T, A.N, n0, A.y);
 }
 
 // ------------------------------------------------------------------- many rows
@@ -262,16 +301,6 @@ struct BlockTile {
   static constexpr int LDS = NS * STAGE > BM * LDO * 2 ? NS * STAGE : BM * LDO * 2;
   static_assert(TN <= G && G % TN == 0, "a wave's columns lie in one weight block");
   static_assert(BM * 8 % NTHR == 0 && BN * 8 % NTHR == 0 && BM < NTHR && BM % (NTHR / 64) == 0, "whole loads a stage");
-};
-
-struct BlockArgs {
-  const uint8_t *xq, *wq;
-  const float *xs, *ws;
-  int64_t T, H, N;
-  int ws_n, ws_g;  // steps of ws from one column block and from one group to the next
-  int64_t xs_t, xs_g;  // and of xs from one token and from one group to the next
-  uint16_t* y;
-  int mt, nt;
 };
 
 // the words of make_rsrc's buffer resource, for assembly
@@ -447,10 +476,9 @@ hipError_t launch_gemm(BlockArgs a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <int NT>
-hipError_t launch_rows(const uint16_t* x, const uint8_t* wq, const float* ws, int T, int64_t H, int64_t N, uint16_t* y,
-                       hipStream_t stream) {
-  block_rows<1, NT><<<(unsigned)((N + 15) / 16), RW * 64, 0, stream>>>(x, wq, ws, T, H, N, y);
+template <int NT, int RW>
+hipError_t launch_codes(const BlockArgs& a, hipStream_t stream) {
+  block_codes<NT, RW><<<(unsigned)((a.N + 15) / 16), RW * 64, 0, stream>>>(a);
   return hipGetLastError();
 }
 
@@ -478,9 +506,8 @@ hipError_t launch_quant_rows_block(const uint16_t* x, int64_t T, int64_t H, uint
 
 hipError_t launch_block_rows(const uint16_t* x, const uint8_t* wq, const float* ws, int T, int64_t H, int64_t N, uint16_t* y,
                              hipStream_t stream) {
-  if (T <= 16) return launch_rows<1>(x, wq, ws, T, H, N, y, stream);
-  if (T <= 32) return launch_rows<2>(x, wq, ws, T, H, N, y, stream);
-  return launch_rows<4>(x, wq, ws, T, H, N, y, stream);
+  block_rows<8><<<(unsigned)((N + 15) / 16), 8 * 64, 0, stream>>>(x, wq, ws, T, H, N, y);
+  return hipGetLastError();
 }
 
 hipError_t launch_block_gemm(const uint8_t* xq, const float* xs, const uint8_t* wq, const float* ws, int64_t T, int64_t H,
@@ -488,6 +515,12 @@ hipError_t launch_block_gemm(const uint8_t* xq, const float* xs, const uint8_t* 
   const int groups = (int)(H / G), nbs = (int)((N + G - 1) / G);
   const BlockArgs a{xq, wq, xs, ws, T, H, N, ws_transposed ? 1 : groups, ws_transposed ? nbs : 1, xs_cols ? 1 : groups,
                     xs_cols ? T : 1, y, 0, 0};
+  // Few rows and columns leave CUs without a 64 x 64 tile, and 16-column workgroups win; with
+  // many columns the tiles cover the chip and read the tokens' codes less often.  16 rows: 12.3
+  // against 13.8 us at N = 8192 (H = 4096), 22 against 19.6 at N = 14336; 32 rows: 14.6 against
+  // 21 at N = 4096 (H = 7168), 9.8 against 8.5 at N = 6144 (H = 2048).
+  if (T <= 16 && N <= 8192) return launch_codes<1, 8>(a, stream);
+  if (T <= 32 && N <= 4096) return launch_codes<2, 8>(a, stream);
   const auto tiles = [&](int64_t bm, int64_t bn) { return ((T + bm - 1) / bm) * ((N + bn - 1) / bn); };
   if (tiles(256, 256) >= 192) return launch_gemm<BlockTile<256, 256, 4, 2, 2>>(a, stream);
   if (tiles(128, 128) >= 192) return launch_gemm<BlockTile<128, 128, 2, 2, 2>>(a, stream);

@@ -352,7 +352,7 @@ hipError_t launch_quant_block(const uint16_t* w, int64_t E, int64_t H, int64_t N
 //   x [T][H] bf16 -> xq [T][H] E4M3, xs [T][H/128], or [H/128][T] with cols
 hipError_t launch_quant_rows_block(const uint16_t* x, int64_t T, int64_t H, uint8_t* xq, float* xs, bool cols,
                                    hipStream_t stream);
-constexpr int BLOCK_MAX_ROWS = 64;  // tokens up to which launch_block_rows takes them
+constexpr int BLOCK_MAX_ROWS = 16;  // tokens up to which launch_block_rows takes them
 //   y [T][N] of bf16 tokens x [T][H], quantised on the way (T <= BLOCK_MAX_ROWS)
 hipError_t launch_block_rows(const uint16_t* x, const uint8_t* wq, const float* ws, int T, int64_t H, int64_t N, uint16_t* y,
                              hipStream_t stream);

@@ -150,7 +150,7 @@ def linear_fp8_block(x, weight):
     [H,N], quantised per block of 128 x 128 in the call (H and N multiples of 128): then the call is differentiable in
     both, dx from the E4M3 codes of dy (per token and 128 of N) and of the weight, dw = x^T dy as a bf16 product, the
     quantisation's own derivative taken as 1.  Or a pair (codes, descale) from quantize_block (serving; N a multiple
-    of 16): no gradient.  At most 64 tokens of a quantised weight take one launch."""
+    of 16): no gradient.  At most 16 tokens of a quantised weight take one launch."""
     check_tensor("x", x, _BF16, (2,))
     H = x.shape[1]
     if isinstance(weight, torch.Tensor):

@@ -68,7 +68,8 @@ def test_quantize_block_bits(E, H, N):
 
 
 @pytest.mark.parametrize("T,H,N", [(1, 128, 16), (1, 2048, 1552), (5, 640, 144), (16, 256, 48), (17, 1152, 272), (33, 256, 1040),
-                                   (64, 384, 32)])
+                                   (64, 384, 32), (16, 128, 8208), (3, 128, 8192), (32, 256, 4096), (32, 128, 4112),
+                                   (16, 1024, 64), (15, 2432, 16)])
 def test_few_rows(T, H, N):
     import mixture_experts_ffn_int32_amd as hmm
     announce("linear_fp8_block few rows %s" % ((T, H, N),))
