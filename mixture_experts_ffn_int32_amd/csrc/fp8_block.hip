@@ -96,27 +96,40 @@ __global__ void __launch_bounds__(QB_THREADS) quant_block(const uint16_t* __rest
 // 16 consecutive lanes hold a group (8 elements each); H / 8 is a multiple of 16, so a
 // group's lanes are active together.
 constexpr int QR_THREADS = 256;
+constexpr int QR_TOKENS = QR_THREADS / 16;
 constexpr int64_t QR_MAX_BLOCKS = 1 << 20;
 
-// COLS: the descales as [H / 128][T], so that the product reads those of a group side by side.
-// (T H / 128 stays below 2^32: the codes alone would not fit the card otherwise.)
-template <bool COLS>
-__global__ void __launch_bounds__(QR_THREADS) quant_rows_block(const uint16_t* __restrict__ x, int64_t chunks, uint32_t groups,
-                                                               uint32_t T, uint8_t* __restrict__ xq, float* __restrict__ xs) {
-  for (int64_t c = (int64_t)blockIdx.x * QR_THREADS + threadIdx.x; c < chunks; c += (int64_t)gridDim.x * QR_THREADS) {
-    float v[8], s[8];
-    unpack8(*reinterpret_cast<const u32x4*>(x + c * 8), v);
-    float m = 0.f;
+// One chunk of a group: its codes at chunk c, and the group's descale.
+__device__ __forceinline__ void quant_chunk(const uint16_t* __restrict__ x, int64_t c, uint8_t* __restrict__ xq,
+                                            float* __restrict__ descale) {
+  float v[8], s[8];
+  unpack8(*reinterpret_cast<const u32x4*>(x + c * 8), v);
+  float m = 0.f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(v[j]));
+  for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(v[j]));
 #pragma unroll
-    for (int d = 8; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor(m, d));
-    const float sc = block_scale_of(m);
+  for (int d = 8; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor(m, d));
+  const float sc = block_scale_of(m);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) s[j] = sc;
-    *reinterpret_cast<uint2*>(xq + c * 8) = to_e4m3x8(v, s);
-    const uint32_t i = (uint32_t)(c >> 4);
-    if ((c & 15) == 0) xs[COLS ? (int64_t)(i % groups) * T + i / groups : (int64_t)i] = 1.f / sc;
+  for (int j = 0; j < 8; ++j) s[j] = sc;
+  *reinterpret_cast<uint2*>(xq + c * 8) = to_e4m3x8(v, s);
+  if ((threadIdx.x & 15) == 0) *descale = 1.f / sc;
+}
+
+// Descales [T][H / 128]: chunks in memory order.
+__global__ void __launch_bounds__(QR_THREADS) quant_rows_block(const uint16_t* __restrict__ x, int64_t chunks,
+                                                               uint8_t* __restrict__ xq, float* __restrict__ xs) {
+  for (int64_t c = (int64_t)blockIdx.x * QR_THREADS + threadIdx.x; c < chunks; c += (int64_t)gridDim.x * QR_THREADS)
+    quant_chunk(x, c, xq, xs + (c >> 4));
+}
+
+// Descales [H / 128][T], so that the product reads those of a group side by side.  A workgroup
+// takes one group of 16 tokens: their descales are one 64-byte line of one L2.
+__global__ void __launch_bounds__(QR_THREADS) quant_cols_block(const uint16_t* __restrict__ x, int64_t T, int groups, int64_t tiles,
+                                                               uint8_t* __restrict__ xq, float* __restrict__ xs) {
+  for (int64_t b = blockIdx.x; b < tiles; b += gridDim.x) {
+    const int64_t g = b % groups, t = b / groups * QR_TOKENS + (threadIdx.x >> 4);
+    if (t < T) quant_chunk(x, (t * groups + g) * 16 + (threadIdx.x & 15), xq, xs + g * T + t);
   }
 }
 
@@ -494,13 +507,14 @@ hipError_t launch_quant_block(const uint16_t* w, int64_t E, int64_t H, int64_t N
 
 hipError_t launch_quant_rows_block(const uint16_t* x, int64_t T, int64_t H, uint8_t* xq, float* xs, bool cols,
                                    hipStream_t stream) {
-  const int64_t chunks = T * (H / 8), blocks = (chunks + QR_THREADS - 1) / QR_THREADS;
-  if (chunks <= 0) return hipSuccess;
+  if (T <= 0) return hipSuccess;
+  const int64_t groups = H / G, chunks = T * (H / 8);
+  const int64_t blocks = cols ? (T + QR_TOKENS - 1) / QR_TOKENS * groups : (chunks + QR_THREADS - 1) / QR_THREADS;
   const unsigned grid = (unsigned)(blocks < QR_MAX_BLOCKS ? blocks : QR_MAX_BLOCKS);
   if (cols)
-    quant_rows_block<true><<<grid, QR_THREADS, 0, stream>>>(x, chunks, (uint32_t)(H / G), (uint32_t)T, xq, xs);
+    quant_cols_block<<<grid, QR_THREADS, 0, stream>>>(x, T, (int)groups, blocks, xq, xs);
   else
-    quant_rows_block<false><<<grid, QR_THREADS, 0, stream>>>(x, chunks, (uint32_t)(H / G), (uint32_t)T, xq, xs);
+    quant_rows_block<<<grid, QR_THREADS, 0, stream>>>(x, chunks, xq, xs);
   return hipGetLastError();
 }
 
