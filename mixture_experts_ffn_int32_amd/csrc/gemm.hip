@@ -346,11 +346,13 @@ static hipError_t launch_dw_dense_tiles(const DwJob& job, hipStream_t stream) {
   const auto a = dw_args<C, false, false>(job);
   return launch<Dw<C, false, false>>(a, dw_blocks(a), stream);
 }
-// The widest tiles that give (nearly) every CU one.  4096 rows, M = 4096, N = 2048: 256 x 256 tiles
-// (128 of them) 103 us, 256 x 128 73 us, 128 x 128 81 us, 64 x 64 136 us.
+// The fewest rounds of the 256 CUs, then the widest tiles.  4096 rows, M = 4096, N = 2048: 256 x 256
+// tiles (128 of them) 103 us, 256 x 128 73 us (941 TFLOP/s; a large library product
+// reaches 1215), 128 x 128 81 us, 64 x 64 136 us.  M = 2560, N = 4096: 160 tiles of 256 x 256 109 us, 320 of
+// 256 x 128 in two rounds 131 us.
 hipError_t launch_dw_dense(const DwJob& job, hipStream_t stream) {
   const auto tiles = [&](int64_t bm, int64_t bn) { return ((job.M + bm - 1) / bm) * ((job.N + bn - 1) / bn); };
-  if (tiles(256, 256) >= 192) return launch_dw_dense_tiles<Big>(job, stream);
+  if (tiles(256, 256) > 128) return launch_dw_dense_tiles<Big>(job, stream);
   if (tiles(256, 128) >= 128) return launch_dw_dense_tiles<Mid>(job, stream);
   return launch_dw_dense_tiles<Narrow>(job, stream);
 }

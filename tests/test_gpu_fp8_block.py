@@ -111,7 +111,8 @@ def test_many_rows(T, H, N):
     assert torch.equal(guard[:T], y) and bool((guard[T] == 7.0).all())
 
 
-@pytest.mark.parametrize("T,H,N", [(1, 128, 128), (7, 384, 256), (64, 256, 640), (300, 256, 384), (1025, 640, 512)])
+@pytest.mark.parametrize("T,H,N", [(1, 128, 128), (7, 384, 256), (64, 256, 640), (300, 256, 384), (1025, 640, 512),
+                                   (77, 2432, 2048), (130, 3200, 2688)])
 def test_gradients(T, H, N):
     """dx of the codes of dy and of the weight, dw of the bf16 product, each against its formula."""
     import mixture_experts_ffn_int32_amd as hmm
