@@ -106,3 +106,38 @@ def test_training_block():
     a, b = first["d_residual"], want["d_residual"]
     tol = 2.0 ** -8 * (np.abs(a[0]) + np.abs(b[0]) + np.abs(a[0] + b[0])) * (1 + 2.0 ** -8) + c * U * (a[1] + b[1])
     assert np.all(np.abs(_f(x.grad) - (a[0] + b[0])) <= tol)
+
+
+@pytest.mark.parametrize("T", [3, 15, 31, 64, 300])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_a_bad_token_stays_alone(T, bad):
+    """A NaN or an infinity in one token: its own outputs are not finite, every other token's bits are as without it."""
+    import mixture_experts_ffn_int32_amd as hmm
+    from test_gpu_decode import _layer
+    H, I, E, K = 256, 128, 6, 2
+    announce("bad token T=%d %s" % (T, bad))
+    x, up, _, _ = _layer(T, H, I, E, 61, False)[:4]
+    g = torch.Generator().manual_seed(62)
+    x, w = x.cuda(), (torch.randn((H, 400), generator=g) * H ** -0.5).bfloat16().cuda()
+    stream, weight = torch.randn((T, H), generator=g).cuda(), torch.ones(H).cuda()
+    ids = torch.rand((T, E), generator=g).argsort(dim=1)[:, :K].int().cuda()
+    tw = torch.full((T, K), 0.5).cuda()
+    ids[T - 2], tw[T - 2] = -1, bad   # a token whose slots are all dropped: zero, whatever its weights
+
+    def run(x):
+        with torch.no_grad():
+            outs = [hmm.linear_fp8_block(x, hmm.quantize_block(w)), *hmm.residual_norm(x, stream, weight),
+                    hmm.matmul_fp8_block(*hmm.quantize_rows_block(x), *hmm.quantize_block(w))]
+            if T <= 64:
+                outs.append(hmm.moe_decode(x, *up, topk_ids=ids, topk_weights=tw))
+                assert not outs[-1][T - 2].any()
+        return outs
+    want = run(x)
+    assert all(bool(torch.isfinite(o).all()) for o in want)
+    b = x.clone()
+    b[T // 2, 130] = bad
+    rest = [t for t in range(T) if t != T // 2]
+    for o, r in zip(run(b), want):
+        assert torch.equal(o[rest], r[rest])
+        if T // 2 != T - 2:
+            assert not bool(torch.isfinite(o[T // 2]).all())

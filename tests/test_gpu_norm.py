@@ -60,6 +60,7 @@ CASES = [
     (130, 2048, "bf16", "bf16", "full", False), (1300, 264, "f32", "f32", "channel", True), (5, 4096, "bf16", "bf16", "none", False),
     (700, 4104, "f32", "f32", "token", False), (3, 8192, "bf16", "bf16", "channel", True), (4, 8200, "f32", "f32", "full", True),
     (2, 16384, "bf16", "bf16", "channel", True), (2500, 96, "bf16", "bf16", "token", True),
+    (2400, 7176, "bf16", "bf16", "token", True),  # outputs past the L2 caches
 ]
 
 
@@ -127,6 +128,23 @@ def test_one_output_used_and_strided_inputs():
         o = hmm.residual_norm(*leaves2, post_weight=v["post_weight"], gate=v["gate"])
         want = torch.autograd.grad(o, leaves2, (v["tr"], zero) if which == 0 else (zero, v["dn"]))
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("T,H,res", [(1100, 7168, torch.bfloat16), (4500, 264, torch.float32), (9, 16384, torch.float32)])
+def test_outputs_over_the_inputs(T, H, res):
+    """residual_out on residual and normed on y, as the C call allows, with more rows than are taken at once."""
+    import ctypes
+    import mixture_experts_ffn_int32_amd as hmm
+    from mixture_experts_ffn_int32_amd import _lib
+    announce("norm in place %s" % ((T, H, res),))
+    v = _inputs(T, H, res, torch.bfloat16, "channel", True, 19)
+    out, n = hmm.residual_norm(v["y"], v["residual"], v["norm_weight"], post_weight=v["post_weight"], gate=v["gate"], eps=1e-5)
+    p = _lib.NormProblem(T, H, _lib.HMM_F32 if res == torch.float32 else _lib.HMM_BF16, _lib.HMM_BF16, _lib.HMM_GATE_CHANNEL,
+                         1e-5, 1.0)
+    a = [ctypes.c_void_p(v[k].data_ptr()) for k in ("y", "residual", "norm_weight", "post_weight", "gate")]
+    _lib.check(_lib.load().hmm_residual_norm(ctypes.byref(p), *a, a[1], a[0], None,
+                                             ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)))
+    assert torch.equal(v["residual"], out) and torch.equal(v["y"], n)
 
 
 def test_no_rows():
