@@ -22,10 +22,10 @@
 // device), then go to the workspace as one partial row per workgroup, and a
 // second launch adds those in order: no atomics, the same bits on every run.
 //
-// Measured: 8192 rows of 7168, bf16: forward 104-117 us for 470 MB (4.0-4.5 TB/s),
-// backward 142-151 us for 705 MB (4.7-5.0 TB/s) and 5 us for the sums; 4001 rows of
+// Measured: 8192 rows of 7168, bf16: forward 85-96 us for 470 MB (4.9-5.5 TB/s),
+// backward 132-142 us for 705 MB (5.0-5.3 TB/s) and 4 us for the sums; 4001 rows of
 // 2048 with a float32 stream: 21 us (98 MB, in part from the L2 caches and the
-// infinity cache), 28 us and 4 us.  A large copy reaches 5.2 TB/s.  One row: 3.9 us.
+// infinity cache), 28 us and 4 us; 16384 rows of 512: 14, 22 and 4 us.  A large copy reaches 5.2 TB/s.  One row: 3.9 us.
 #include "device.h"
 #include "kernels.h"
 
@@ -366,21 +366,41 @@ __global__ void __launch_bounds__(NT == 64 ? 256 : NT) residual_norm_bwd(const N
     if constexpr (AHEAD) R = N;
   }
 
-  // one partial row per row walker: dw, then dwp, then dg (those that are asked for)
-  const int64_t pr = (int64_t)blockIdx.x * RPB + slot, np = (int64_t)gridDim.x * RPB;
+  // one partial row per workgroup: dw, then dwp, then dg (those that are asked for)
+  float* p = G.partial + (int64_t)blockIdx.x * A.H;
+  const int64_t next = (int64_t)gridDim.x * A.H;
+  auto put = [&](const float (&c)[V][8]) {
+    if constexpr (RPB > 1) {  // the waves' sums in LDS first, added in the waves' order
+      __shared__ __attribute__((aligned(16))) float waves[RPB][NT * V * 8];
+      __syncthreads();  // the previous array has been read
 #pragma unroll
-  for (int k = 0; k < V; ++k) {
-    const int64_t i = (int64_t)(tid + k * NT) * 8;
-    if (i >= A.H) continue;
-    float* p = G.partial + pr * A.H + i;
-    store8(p, true, 0, cw[k]);
-    p += np * A.H;
-    if (A.post_weight) {
-      store8(p, true, 0, cp[k]);
-      p += np * A.H;
+      for (int k = 0; k < V; ++k) store8(waves[slot], true, (tid + k * NT) * 8, c[k]);
+      __syncthreads();
+      const int i = threadIdx.x * 8;
+      if (threadIdx.x < NT * V && i < A.H) {
+        float s[8], v[8];
+        load8(waves[0], true, i, s);
+#pragma unroll
+        for (int q = 1; q < RPB; ++q) {
+          load8(waves[q], true, i, v);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) s[j] += v[j];
+        }
+        store8(p, true, i, s);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        const int64_t i = (int64_t)(tid + k * NT) * 8;
+        if (i < A.H) store8(p, true, i, c[k]);
+      }
     }
-    if constexpr (CHAN) store8(p, true, 0, cg[k]);
-  }
+    p += next;
+  };
+  static_assert(RPB == 1 || NT * V <= NT * RPB, "a thread for each chunk");
+  put(cw);
+  if (A.post_weight) put(cp);
+  if constexpr (CHAN) put(cg);
 }
 
 // out[c] = sum of the np partial rows of column c, in order: 16 row groups of 64
@@ -410,20 +430,25 @@ __global__ void __launch_bounds__(64 * PS_GROUPS) norm_partial_sum(const float* 
     static_cast<uint16_t*>(out)[c] = f2bf(s);
 }
 
-// calls f<threads per row, chunks per thread> for rows of H elements
+// Calls f<threads per row, chunks per thread> for rows of H elements.  Few waves a row, so that
+// several rows overlap on a CU, as far as registers hold a row and the next one.  Forward /
+// backward of 8192 rows of 7168: 512 threads 85 / 132 us, 1024 106 / 140, 256 100 / 162; of 4096:
+// 256 threads 48 / 74, 512 52 / 72, 128 59 / 92; of 2048: 256 threads 25 / 40, 128 26 / 50; 2000
+// rows of 16384: 1024 threads 52 / 160, 512 54 / 144.
 template <class F>
 hipError_t for_width(int64_t H, F&& f) {
   if (H <= 512) return f.template operator()<64, 1>();
   if (H <= 1024) return f.template operator()<64, 2>();
   if (H <= 2048) return f.template operator()<256, 1>();
-  if (H <= 4096) return f.template operator()<512, 1>();
-  if (H <= 8192) return f.template operator()<1024, 1>();
-  return f.template operator()<1024, 2>();
+  if (H <= 4096) return f.template operator()<256, 2>();
+  if (H <= 8192) return f.template operator()<512, 2>();
+  return f.template operator()<F::LONGEST, 2048 / F::LONGEST>();
 }
 
 // Threads of a forward launch: as many as the 256 CUs hold.  Each row walker takes rows in turn.
 constexpr int FWD_THREADS = 1 << 19;
 struct FwdLaunch {
+  static constexpr int LONGEST = 1024;  // threads of rows above 8192
   const NormArgs& A;
   hipStream_t stream;
   template <int NT, int V, bool RF, bool WF>
@@ -442,6 +467,7 @@ struct FwdLaunch {
   }
 };
 struct BwdLaunch {
+  static constexpr int LONGEST = 512;
   const NormArgs& A;
   const NormGradArgs& G;
   int blocks;
@@ -464,18 +490,19 @@ struct BwdLaunch {
   }
 };
 
-// Row walkers of the backward, each with one partial row: 1024 waves or 512 workgroups of
-// up to 512 threads (two a CU), 256 of 1024.  8192 rows of 7168: 256 of them 141 us and 5 us
-// for their sums, 512 148 + 14, 1024 159 + 25; 4001 rows of 2048: 512 27 + 8, 256 35 + 5.
+// Workgroups of the backward, each with one partial row: 512, or 256 of 512 threads (their
+// registers allow two waves a SIMD).  8192 rows of 7168: 256 of them 132 us and 4 us for their
+// sums, 512 136 + 6; 4001 rows of 2048: 512 27 + 4, 256 35 + 3; 16384 rows of 512: 256 28 + 4,
+// 512 22 + 4, 1024 24 + 5.
 inline int bwd_blocks(int64_t T, int64_t H) {
   const int64_t rpb = H <= 1024 ? 4 : 1;
-  const int64_t b = (T + rpb - 1) / rpb, most = H <= 1024 ? 1024 / 4 : H <= 4096 ? 512 : 256;
+  const int64_t b = (T + rpb - 1) / rpb, most = H <= 4096 ? 512 : 256;
   return (int)(b < most ? b : most);
 }
 
 }  // namespace
 
-int64_t norm_partial_rows(int64_t T, int64_t H) { return (int64_t)bwd_blocks(T, H) * (H <= 1024 ? 4 : 1); }
+int64_t norm_partial_rows(int64_t T, int64_t H) { return bwd_blocks(T, H); }
 
 // Outputs past the L2 caches' 32 MB are stored with the streaming hint (8192 rows of 7168,
 // backward: 144 us with it, 154 without).
