@@ -28,7 +28,7 @@
 // way a token's rows are added in the order of its slots: the same bits on every run.
 //
 // Measured, bf16, E = 32, H = 7168, I = 2048, K = 8: 1 token: logits 4.7, top-k 4.9, up 88 us
-// (470 MB: 5.3 TB/s), down 47 us (235 MB: 5.0 TB/s); 64 tokens: 7, 5, 334 us (1880 MB: 5.6
+// (470 MB: 5.3 TB/s), down 47 us (235 MB: 5.0 TB/s); 64 tokens: 6, 5, 334 us (1880 MB: 5.6
 // TB/s), 199 us (940 MB: 4.7 TB/s), sum 6 us.  E = 128, H = 2048, I = 768, 17 tokens: up 94, down
 // 57 us (5.4 and 4.5 TB/s).  E4M3 weights, 8 tokens: up 141 us (5.6 TB/s), down 95 us (4.2
 // TB/s).  Reads alone reach 6.2 TB/s here, a copy 5.2.
@@ -47,8 +47,9 @@ static_assert(DT == 64, "the rows of an expert are one 64-bit lane mask");
 
 // ------------------------------------------------------------------------ router
 
-// logits[t][e] in float64: a workgroup takes GE experts and GT tokens, its
-// threads split H in 16-byte chunks.
+// logits[t][e] in float64: a workgroup takes one expert and GT tokens, its threads split H in
+// 16-byte chunks.  Latency counts: 64 tokens, 32 experts, H = 7168 5.6 us with GT = 4, 5.3 with 2,
+// 6.2 with two experts a workgroup; 256 experts 24, 26 and 23 us.
 constexpr int GTHR = 512;
 
 template <class W>
@@ -71,40 +72,34 @@ __device__ __forceinline__ void router8<float>(const float* p, double (&v)[8]) {
   }
 }
 
-template <class W, int GE, int GT>
+template <class W, int GT>
 __global__ void __launch_bounds__(GTHR) router_logits(const uint16_t* __restrict__ x, const W* __restrict__ wr, int T,
                                                       int64_t H, int E, double* __restrict__ logits) {
-  __shared__ double part[GTHR / 64][GE * GT];
-  const int e0 = blockIdx.x * GE, t0 = blockIdx.y * GT;
-  double acc[GE][GT] = {};
+  __shared__ double part[GTHR / 64][GT];
+  const int e = blockIdx.x, t0 = blockIdx.y * GT;
+  double acc[GT] = {};
   for (int64_t c = (int64_t)threadIdx.x * 8; c < H; c += GTHR * 8) {
     double xv[GT][8], wv[8];
 #pragma unroll
     for (int t = 0; t < GT; ++t) router8<uint16_t>(x + (int64_t)min(t0 + t, T - 1) * H + c, xv[t]);
+    router8<W>(wr + (int64_t)e * H + c, wv);
 #pragma unroll
-    for (int e = 0; e < GE; ++e) {
-      router8<W>(wr + (int64_t)min(e0 + e, E - 1) * H + c, wv);
+    for (int t = 0; t < GT; ++t)
 #pragma unroll
-      for (int t = 0; t < GT; ++t)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) acc[e][t] = __builtin_fma(xv[t][j], wv[j], acc[e][t]);
-    }
+      for (int j = 0; j < 8; ++j) acc[t] = __builtin_fma(xv[t][j], wv[j], acc[t]);
   }
 #pragma unroll
-  for (int e = 0; e < GE; ++e)
+  for (int t = 0; t < GT; ++t) {
 #pragma unroll
-    for (int t = 0; t < GT; ++t) {
-#pragma unroll
-      for (int d = 32; d >= 1; d >>= 1) acc[e][t] += __shfl_xor(acc[e][t], d);
-      if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6][e * GT + t] = acc[e][t];
-    }
+    for (int d = 32; d >= 1; d >>= 1) acc[t] += __shfl_xor(acc[t], d);
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6][t] = acc[t];
+  }
   __syncthreads();
-  if (threadIdx.x < GE * GT) {
-    const int e = e0 + threadIdx.x / GT, t = t0 + threadIdx.x % GT;
+  if (threadIdx.x < GT && t0 + threadIdx.x < T) {
     double s = 0.;
 #pragma unroll
     for (int q = 0; q < GTHR / 64; ++q) s += part[q][threadIdx.x];
-    if (e < E && t < T) logits[(int64_t)t * E + e] = s;
+    logits[(int64_t)(t0 + threadIdx.x) * E + e] = s;
   }
 }
 
@@ -675,13 +670,12 @@ __global__ void __launch_bounds__(DW * 64, 2) decode_down(const DecodeArgs A) {
   }
 }
 
-// one token: a workgroup per expert (four tokens would only repeat it)
 template <class W>
 void launch_logits(const uint16_t* x, const W* wr, int T, int64_t H, int E, double* logits, hipStream_t stream) {
-  if (T == 1)
-    router_logits<W, 1, 1><<<E, GTHR, 0, stream>>>(x, wr, T, H, E, logits);
+  if (T == 1)  // four tokens would only repeat it
+    router_logits<W, 1><<<E, GTHR, 0, stream>>>(x, wr, T, H, E, logits);
   else
-    router_logits<W, 2, 4><<<dim3((E + 1) / 2, (T + 3) / 4), GTHR, 0, stream>>>(x, wr, T, H, E, logits);
+    router_logits<W, 4><<<dim3(E, (T + 3) / 4), GTHR, 0, stream>>>(x, wr, T, H, E, logits);
 }
 
 template <class WT, int NT, int DW, bool WIDE>

@@ -433,12 +433,14 @@ __global__ void __launch_bounds__(64 * PS_GROUPS) norm_partial_sum(const float* 
 // Calls f<threads per row, chunks per thread> for rows of H elements.  Few waves a row, so that
 // several rows overlap on a CU, as far as registers hold a row and the next one.  Forward /
 // backward of 8192 rows of 7168: 512 threads 85 / 132 us, 1024 106 / 140, 256 100 / 162; of 4096:
-// 256 threads 48 / 74, 512 52 / 72, 128 59 / 92; of 2048: 256 threads 25 / 40, 128 26 / 50; 2000
+// 256 threads 48 / 74, 512 52 / 72, 128 59 / 92; of 2048: 256 threads 25 / 40, 128 26 / 50;
+// 32000 of 1408: 192 threads 76 / 118, 256 84 / 137 us; 2000
 // rows of 16384: 1024 threads 52 / 160, 512 54 / 144.
 template <class F>
 hipError_t for_width(int64_t H, F&& f) {
   if (H <= 512) return f.template operator()<64, 1>();
   if (H <= 1024) return f.template operator()<64, 2>();
+  if (H <= 1536) return f.template operator()<192, 1>();
   if (H <= 2048) return f.template operator()<256, 1>();
   if (H <= 4096) return f.template operator()<256, 2>();
   if (H <= 8192) return f.template operator()<512, 2>();
@@ -490,13 +492,13 @@ struct BwdLaunch {
   }
 };
 
-// Workgroups of the backward, each with one partial row: 512, or 256 of 512 threads (their
-// registers allow two waves a SIMD).  8192 rows of 7168: 256 of them 132 us and 4 us for their
-// sums, 512 136 + 6; 4001 rows of 2048: 512 27 + 4, 256 35 + 3; 16384 rows of 512: 256 28 + 4,
+// Workgroups of the backward, each with one partial row: 512 (of 256 threads with two chunks
+// each: two waves a SIMD, as the registers allow), 768 of one chunk (three), 256 of 512 threads.
+// 8192 rows of 7168: 256 of them 132 us and 4 us for their sums, 512 136 + 6; 16000 rows of 2048: 768 74 + 4, 512 84 + 4; 16384 rows of 512: 256 28 + 4,
 // 512 22 + 4, 1024 24 + 5.
 inline int bwd_blocks(int64_t T, int64_t H) {
   const int64_t rpb = H <= 1024 ? 4 : 1;
-  const int64_t b = (T + rpb - 1) / rpb, most = H <= 4096 ? 512 : 256;
+  const int64_t b = (T + rpb - 1) / rpb, most = H > 4096 ? 256 : H > 1024 && H <= 2048 ? 768 : 512;
   return (int)(b < most ? b : most);
 }
 

@@ -60,6 +60,7 @@ CASES = [
     (130, 2048, "bf16", "bf16", "full", False), (1300, 264, "f32", "f32", "channel", True), (5, 4096, "bf16", "bf16", "none", False),
     (700, 4104, "f32", "f32", "token", False), (3, 8192, "bf16", "bf16", "channel", True), (4, 8200, "f32", "f32", "full", True),
     (2, 16384, "bf16", "bf16", "channel", True), (2500, 96, "bf16", "bf16", "token", True),
+    (6, 1536, "bf16", "f32", "full", True), (900, 1544, "f32", "bf16", "channel", True), (2100, 504, "bf16", "bf16", "channel", True),
     (2400, 7176, "bf16", "bf16", "token", True),  # outputs past the L2 caches
 ]
 
