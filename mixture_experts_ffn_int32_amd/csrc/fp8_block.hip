@@ -144,7 +144,8 @@ __global__ void __launch_bounds__(QR_THREADS) quant_cols_block(const uint16_t* _
 // ------------------------------------------------------------------- few rows
 // Bound by the weight's bytes, and below a few tens of megabytes by the latency of its one round
 // of loads.  A workgroup owns 16 columns; its RW waves take the groups in
-// turn, streaming codes from global memory into two register sets, and add their sums up in LDS
+// turn, streaming codes from global memory into two register sets (six: 12.7 us where two take
+// 10.4), and add their sums up in LDS
 // at the end.  Lane l holds 32 codes of a group, k = 32 (l / 16) + 0.., of weight row and of
 // token l % 16.
 struct BlockArgs {
