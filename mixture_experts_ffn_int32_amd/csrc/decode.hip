@@ -29,8 +29,8 @@
 //
 // Measured, bf16, E = 32, H = 7168, I = 2048, K = 8: 1 token: logits 4.7, top-k 4.9, up 88 us
 // (470 MB: 5.3 TB/s), down 47 us (235 MB: 5.0 TB/s); 64 tokens: 6, 5, 334 us (1880 MB: 5.6
-// TB/s), 199 us (940 MB: 4.7 TB/s), sum 6 us.  E = 128, H = 2048, I = 768, 17 tokens: up 94, down
-// 57 us (5.4 and 4.5 TB/s).  E4M3 weights, 8 tokens: up 141 us (5.6 TB/s), down 95 us (4.2
+// TB/s), 199 us (940 MB: 4.7 TB/s), sum 6 us.  E = 128, H = 2048, I = 768, 17 tokens: up 89, down
+// 47 us (5.7 and 5.4 TB/s).  E4M3 weights, 8 tokens: up 141 us (5.6 TB/s), down 95 us (4.2
 // TB/s).  Reads alone reach 6.2 TB/s here, a copy 5.2.
 #include "gemm_common.h"
 #include "kernels.h"
@@ -691,15 +691,18 @@ void launch_down(const DecodeArgs& A, int64_t act, hipStream_t stream) {
 
 constexpr int SUM_TOKENS = 4;  // up to which the down-projection adds the rows up (both sides: launch_experts)
 
-// WA: weights of up to 16 tokens (one row tile), WB: of more.  Wide tiles (a wave's 128 columns
-// side by side) where they still give every workgroup a unit: up-projection of 32 experts, H =
-// 7168, I = 2048, 64 tokens 332 us wide, 371 narrow; 86 chosen experts, H = 2048, I = 768, 17
-// tokens 91 / 95; down-projection of the latter 56 / 61, of the former 200 / 198.  With E4M3
-// weights wide tiles gained nothing (93 / 89).
+// WA: one row tile at a time, for experts with up to 16 rows (with more, the tile is read again for
+// the next 16); WB: two.  One where an expert has 8 rows or fewer on average: up + down of 17 tokens,
+// 128 experts, K = 8 (1 row) 89 + 47 us against 93 + 57; 64 tokens, 64 E4M3 experts, K = 8 (8 rows)
+// 73 + 49 against 88 + 53; but 64 tokens, 32 experts, K = 6 (12 rows) 409 + 200 against 329 + 190.
+// Wide tiles (a wave's 128 columns side by side) where they still give every workgroup a unit:
+// up-projection of 32 experts, H = 7168, I = 2048, 64 tokens 332 us wide, 371 narrow; 86 chosen
+// experts, H = 2048, I = 768, 17 tokens 91 / 95; down-projection of the latter 56 / 61, of the
+// former 200 / 198.  With E4M3 weights wide tiles gained nothing (93 / 89).
 template <class WA, class WB, int DW>
 hipError_t launch_experts(const DecodeArgs& A, hipStream_t stream) {
   const int64_t act = A.E < A.T * A.K ? A.E : A.T * A.K;  // experts that may be chosen
-  const bool few = A.T <= 16;
+  const bool few = A.T <= 16 || A.T * A.K <= 8 * A.E;
   bool up = false, down = false;
   if constexpr (WA::WIDE) {
     if (A.I % WA::COLS == 0 && act * (A.I / WA::COLS) >= MAX_GROUPS) {

@@ -65,7 +65,7 @@ SHAPES = [  # T, H, I, E, K, fp8
     (16, 256, 192, 33, 8, False), (17, 448, 64, 7, 2, False), (32, 320, 128, 3, 3, False), (33, 128, 192, 6, 1, False),
     (64, 256, 128, 4, 4, False), (64, 576, 64, 70, 8, False), (2, 128, 64, 1024, 16, False),
     # wide tiles of both projections, with a last column tile of 64, for one and for two row tiles
-    (16, 1088, 512, 128, 8, False), (64, 1088, 512, 128, 8, False),
+    (16, 1088, 512, 128, 8, False), (64, 1088, 512, 128, 8, False), (64, 1344, 640, 120, 16, False),
     (1, 128, 128, 1, 1, True), (5, 512, 128, 4, 2, True), (16, 256, 384, 9, 4, True), (23, 640, 128, 5, 3, True),
     (64, 384, 256, 6, 6, True), (48, 256, 128, 40, 2, True),
 ]
@@ -82,6 +82,20 @@ def test_given_routing(T, H, I, E, K, fp8):
     y = hmm.moe_decode(x.cuda(), *weights, topk_ids=ids.cuda(), topk_weights=w.cuda(), **scales)
     torch.cuda.synchronize()
     _check(y, x, ids.numpy(), w.numpy().astype(np.float64), ref, H, I)
+
+
+@pytest.mark.parametrize("T,H,I,E,fp8", [(64, 192, 128, 40, False), (50, 256, 128, 40, True), (64, 1088, 512, 128, False)])
+def test_crowded_expert(T, H, I, E, fp8):
+    """Many experts, so that few rows each are expected, and all tokens go to two of them."""
+    import mixture_experts_ffn_int32_amd as hmm
+    announce("moe_decode crowded expert %s" % ((T, H, I, E, fp8),))
+    x, weights, scales, ref = _layer(T, H, I, E, 31, fp8)
+    g = torch.Generator().manual_seed(32)
+    ids = torch.tensor([[E - 1, 3]]).repeat(T, 1).int()
+    ids[1] = torch.tensor([5, 3])
+    w = torch.rand((T, 2), generator=g)
+    y = hmm.moe_decode(x.cuda(), *weights, topk_ids=ids.cuda(), topk_weights=w.cuda(), **scales)
+    _check(y, x, ids.numpy(), w.numpy(), ref, H, I)
 
 
 @pytest.mark.parametrize("fp8", [False, True])
