@@ -320,16 +320,20 @@ __global__ void __launch_bounds__(RW * 64) block_codes(const BlockArgs A) {
 // 16-byte chunk c sits at position c ^ (row / 2 % 8), so the 16-byte reads of 16 consecutive
 // rows cover every bank once.  (The loads write LDS in lane order, so the permutation is applied to the
 // global address, inside one 128-byte line.)
-template <int BM_, int BN_, int WM_, int WN_, int NS_>
+// KS parts of the workgroup take the steps in turn, each with stages of its own, and their sums are
+// added at the end (part 0 first).
+template <int BM_, int BN_, int WM_, int WN_, int NS_, int KS_>
 struct BlockTile {
   static constexpr int SPREAD = 5;  // tiles of a step that its stage loads are spread over
-  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NS = NS_, NTHR = WM * WN * 64;
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NS = NS_, KS = KS_;
+  static constexpr int HT = WM * WN * 64, NTHR = KS * HT;  // threads of a part, of the workgroup
   static constexpr int TM = BM / WM, TN = BN / WN, MB = TM / 32, NB = TN / 32;
   static constexpr int STAGE = (BM + BN) * G + BM * 4;  // weight rows, token rows, token scales
   static constexpr int LDO = BN + 8;  // output tile pitch, elements
-  static constexpr int LDS = NS * STAGE > BM * LDO * 2 ? NS * STAGE : BM * LDO * 2;
+  static constexpr int LDS = KS * NS * STAGE > BM * LDO * 2 ? KS * NS * STAGE : BM * LDO * 2;
   static_assert(TN <= G && G % TN == 0, "a wave's columns lie in one weight block");
-  static_assert(BM * 8 % NTHR == 0 && BN * 8 % NTHR == 0 && BM < NTHR && BM % (NTHR / 64) == 0, "whole loads a stage");
+  static_assert(BM * 8 % HT == 0 && BN * 8 % HT == 0 && BM < HT && BM % (HT / 64) == 0, "whole loads a stage");
+  static_assert(KS == 1 || BM * BN * 4 <= LDS, "the second part's sums fit");
 };
 
 // the words of make_rsrc's buffer resource, for assembly
@@ -376,7 +380,8 @@ __global__ void __launch_bounds__(C::NTHR) block_gemm(const BlockArgs A) {
   raster(logical, A.mt, A.nt, mt, nt);
   const int64_t m0 = (int64_t)mt * C::BM, n0 = (int64_t)nt * C::BN;
   const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int waves = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int part = waves / (C::HT / 64), wave = waves % (C::HT / 64), tid = threadIdx.x % C::HT;
   const int wm = wave / C::WN, wn = wave % C::WN;
   const int half = lane >> 5, l32 = lane & 31;
   const uint32_t pitch = (uint32_t)A.H;
@@ -394,13 +399,14 @@ __global__ void __launch_bounds__(C::NTHR) block_gemm(const BlockArgs A) {
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[nb][mb][r] = 0.f;
 
-  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)smem;
+  const uint8_t* mine = smem + part * C::NS * C::STAGE;  // the part's stages
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)smem + part * C::NS * C::STAGE;
   // A load takes 8 lanes a row, so the workgroup's i-th one starts RPL rows (a multiple of 16,
   // the permutation's period) further: one offset register serves all of them, and both operands.
-  constexpr int RPL = C::NTHR / 8, LW = C::BN / RPL, LOADS = LW + C::BM / RPL;
+  constexpr int RPL = C::HT / 8, LW = C::BN / RPL, LOADS = LW + C::BM / RPL;
   static_assert(RPL % 16 == 0, "permutation period");
-  const uint32_t voff = (threadIdx.x >> 3) * pitch + (((threadIdx.x & 7) ^ ((threadIdx.x >> 4) & 7)) * 16);
-  constexpr int TPW = C::BM * 64 / C::NTHR;  // tokens whose scales a wave loads
+  const uint32_t voff = (tid >> 3) * pitch + (((tid & 7) ^ ((tid >> 4) & 7)) * 16);
+  constexpr int TPW = C::BM * 64 / C::HT;  // tokens whose scales a wave loads
   const uint32_t soff = (uint32_t)min((int64_t)(wave * TPW + lane), A.T - 1 - m0) * (uint32_t)A.xs_t * 4;
   // Loads [from, to) of stage g into its buffer (past the last stage: of the last one again,
   // unused); the last of them is the scales', BM / waves tokens a wave.  Rows past the tensors' ends are
@@ -411,7 +417,7 @@ __global__ void __launch_bounds__(C::NTHR) block_gemm(const BlockArgs A) {
 #pragma unroll
     for (int i = from; i < to; ++i)
       if (i < LOADS)
-        load_lds16(i < LW ? rw : rx, at + (uint32_t)(i * C::NTHR + wave * 64) * 16,
+        load_lds16(i < LW ? rw : rx, at + (uint32_t)(i * C::HT + wave * 64) * 16,
                    voff + (uint32_t)(i < LW ? i : i - LW) * RPL * pitch, (uint32_t)gc * G);
       else
         load_lds4(rs, at + (C::BM + C::BN) * G + (uint32_t)wave * TPW * 4, soff, (uint32_t)(gc * A.xs_g) * 4, (1ull << TPW) - 1);
@@ -419,19 +425,20 @@ __global__ void __launch_bounds__(C::NTHR) block_gemm(const BlockArgs A) {
   constexpr int TILES = C::NB * C::MB, ALL = LOADS + 1, OVER = C::SPREAD < TILES ? C::SPREAD : TILES;
   constexpr int PER = (ALL + OVER - 1) / OVER;
 #pragma unroll
-  for (int q = 0; q < C::NS - 1; ++q) stage(q, q, 0, ALL);
-  // the block's scales: lane l holds that of group g0 + l, reloaded every 64 groups
+  for (int q = 0; q < C::NS - 1; ++q) stage(q * C::KS + part, q, 0, ALL);
+  // the block's scales: lane l holds that of the part's step i0 + l, reloaded every 64 steps
   float wl = 0.f;
   int buf = 0, fill = C::NS - 1;
-  for (int g = 0; g < groups; ++g) {
-    if ((g & 63) == 0) {
-      wl = wsp[(int64_t)min(g + lane, groups - 1) * A.ws_g];
+  for (int step = 0; step * C::KS < groups; ++step) {
+    const bool live = C::KS == 1 || step * C::KS + part < groups;  // false in an odd last step of part 1
+    if ((step & 63) == 0) {
+      wl = wsp[(int64_t)min((step + lane) * C::KS + part, groups - 1) * A.ws_g];
       asm volatile("" : "+v"(wl));  // waits for it here, once in 64 steps
     }
-    // stage g has landed (NS - 2 later ones may be on their way), and stage g - 1 is done with
+    // this step's stage has landed (NS - 2 later ones may be on their way), and the last one is done with
     asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"i"((C::NS - 2) * ALL) : "memory");
-    const float sw = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, wl), g & 63));
-    const uint8_t* sw_ = smem + buf * C::STAGE;
+    const float sw = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, wl), step & 63));
+    const uint8_t* sw_ = mine + buf * C::STAGE;
     const uint8_t* sx_ = sw_ + C::BN * G;
     const float* ss_ = reinterpret_cast<const float*>(sx_ + C::BM * G);
     i32x8 fb[C::MB][2], fa[2][2];
@@ -459,9 +466,9 @@ __global__ void __launch_bounds__(C::NTHR) block_gemm(const BlockArgs A) {
         t[i & 1] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fa[nb & 1][0], fb[mb][0], zero, 0, 0, 0, 127, 0, 127);
         t[i & 1] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fa[nb & 1][1], fb[mb][1], t[i & 1], 0, 0, 0, 127, 0, 127);
         __builtin_amdgcn_sched_barrier(0);
-        stage(g + C::NS - 1, fill, min(i * PER, ALL), min((i + 1) * PER, ALL));
+        stage((step + C::NS - 1) * C::KS + part, fill, min(i * PER, ALL), min((i + 1) * PER, ALL));
       }
-      if (i > 0) {
+      if (i > 0 && live) {
         const int pn = (i - 1) / C::MB, pm = (i - 1) % C::MB;
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[pn][pm][r] = __builtin_fmaf(s[pm], t[(i - 1) & 1][r], acc[pn][pm][r]);
@@ -473,6 +480,17 @@ __global__ void __launch_bounds__(C::NTHR) block_gemm(const BlockArgs A) {
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the loads past the last stage write into LDS
   __syncthreads();
+  if constexpr (C::KS == 2) {  // part 1's sums through LDS, added by part 0
+    float* sums = reinterpret_cast<float*>(smem) + wave * (C::NB * C::MB * 16 * 64) + lane;
+    if (part == 1)
+#pragma unroll
+      for (int i = 0; i < C::NB * C::MB * 16; ++i) sums[i * 64] = acc[i / 16 / C::MB][i / 16 % C::MB][i % 16];
+    __syncthreads();
+    if (part == 0)
+#pragma unroll
+      for (int i = 0; i < C::NB * C::MB * 16; ++i) acc[i / 16 / C::MB][i / 16 % C::MB][i % 16] += sums[i * 64];
+    __syncthreads();
+  }
   // the tile in bf16 through LDS, so that stores are rows of 16-byte chunks
   uint16_t* out = reinterpret_cast<uint16_t*>(smem);
 #pragma unroll
@@ -480,7 +498,7 @@ __global__ void __launch_bounds__(C::NTHR) block_gemm(const BlockArgs A) {
 #pragma unroll
     for (int mb = 0; mb < C::MB; ++mb)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
+      for (int q = 0; q < 4 && part == 0; ++q) {
         uint2 v;
         v.x = (uint32_t)f2bf(acc[nb][mb][4 * q]) | ((uint32_t)f2bf(acc[nb][mb][4 * q + 1]) << 16);
         v.y = (uint32_t)f2bf(acc[nb][mb][4 * q + 2]) | ((uint32_t)f2bf(acc[nb][mb][4 * q + 3]) << 16);
@@ -557,9 +575,13 @@ hipError_t launch_block_gemm(const uint8_t* xq, const float* xs, const uint8_t* 
   // take 53.9 us against 68.6 of 320 of 256 x 128 in two (5000 x 4096 x 2048); 128 against 256 leave
   // half of the chip idle, 52 to 40 us (4096 x 4096 x 2048).  Below 128 of those, smaller tiles:
   // 28 against 32.6 us (1536 x 4096 x 2048), at 128 still 35.8 against 34.3 (1024 x 4096 x 4096).
-  if (tiles(256, 256) > 128) return launch_gemm<BlockTile<256, 256, 4, 2, 2>>(a, stream);
-  if (tiles(256, 128) >= 128) return launch_gemm<BlockTile<256, 128, 4, 2, 3>>(a, stream);
-  return launch_gemm<BlockTile<64, 64, 2, 2, 3>>(a, stream);
+  if (tiles(256, 256) > 128) return launch_gemm<BlockTile<256, 256, 4, 2, 2, 1>>(a, stream);
+  if (tiles(256, 128) >= 128) return launch_gemm<BlockTile<256, 128, 4, 2, 3, 1>>(a, stream);
+  // Small tiles: up to one a CU, two parts of a workgroup share a tile's groups (64 x 7168 x 4096
+  // 17.9 us against 21.7, 130 x 2048 x 2048 7.6 against 9.1); with more, two workgroups a CU overlap
+  // as well and the parts only cost LDS (1003 x 2048 x 1552, 400 tiles: 14.8 against 11.3).
+  if (tiles(64, 64) <= 256) return launch_gemm<BlockTile<64, 64, 2, 2, 3, 2>>(a, stream);
+  return launch_gemm<BlockTile<64, 64, 2, 2, 3, 1>>(a, stream);
 }
 
 }  // namespace hmm

@@ -87,9 +87,10 @@ def test_few_rows(T, H, N):
 
 
 @pytest.mark.parametrize("T,H,N", [(65, 128, 16), (130, 256, 144), (300, 640, 528), (1003, 256, 1552), (1800, 384, 1808),
-                                   (3400, 256, 3600), (2000, 128, 128), (1900, 384, 2064), (2100, 128, 2064), (4000, 768, 1040)])
+                                   (3400, 256, 3600), (2000, 128, 128), (1900, 384, 2064), (2100, 128, 2064), (4000, 768, 1040),
+                                   (70, 128, 4096), (250, 1152, 1040), (90, 8320, 272)])
 def test_many_rows(T, H, N):
-    """The tiles of 64, 256 x 128 and 256 with ragged edges both ways."""
+    """The tiles of 64 (in one and in two parts), 256 x 128 and 256 with ragged edges both ways."""
     import mixture_experts_ffn_int32_amd as hmm
     announce("linear_fp8_block %s" % ((T, H, N),))
     x, w = _rand((T, H), 3), _rand((H, N), 4)
