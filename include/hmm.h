@@ -465,7 +465,7 @@ hmm_status hmm_moe_decode(const hmm_decode_problem* p, const void* x, const void
  * hmm_quant_block:
  *   y[t,n] = sum_g xs[t,g] descale[n/128,g] sum_{k in g} xq[t,k] codes_t[n,k]
  * Each group's sums are taken by the matrix instruction, scaled in float32 and added in
- * group order; y is bf16, rounded once.
+ * an order that the sizes fix; y is bf16, rounded once.
  *
  * The rule of both quantisers, per group or block: scale = 448 * (1 / max|v|), the
  * reciprocal and the product each rounded to float32 (1 for an all-zero one, at most the

@@ -6,7 +6,8 @@
 // Both operands are stored with the contraction contiguous.  A block is 128 x 128 both
 // ways, so the codes of W [H,N] transposed serve the forward and, as they are, the
 // gradient dx = dy W^T with the same scales.  Each group's sums start from zero, are
-// scaled once by xs ws in float32 and added in group order.
+// scaled once by xs ws in float32 and added in group order (by each of the waves or parts that
+// share a column tile's groups, whose sums are then added in their order).
 //
 // In every kernel the weight is the matrix instruction's first operand (its rows are
 // the output's columns) and the tokens the second, so that a lane of the accumulator
@@ -316,8 +317,8 @@ __global__ void __launch_bounds__(RW * 64) block_codes(const BlockArgs A) {
 // 32x32x64 instructions of a tile, hence the interleaving).  The 16x16x128 instruction, with the
 // scaling of its shorter sums, was slower: 238 us against 202 at 8192 x 7168 x 4096.
 // BM tokens by BN columns a workgroup, one group of 128 a step, NS stages of LDS filled
-// by loads that bypass the registers (the tokens' scales among them).  A row of a stage is 128 bytes, half of the banks; its
-// 16-byte chunk c sits at position c ^ (row / 2 % 8), so the 16-byte reads of 16 consecutive
+// by loads that bypass the registers (the tokens' scales among them).  A row of a stage is 128
+// bytes, half of the banks; its 16-byte chunk c sits at position c ^ (row / 2 % 8), so the 16-byte reads of 16 consecutive
 // rows cover every bank once.  (The loads write LDS in lane order, so the permutation is applied to the
 // global address, inside one 128-byte line.)
 // KS parts of the workgroup take the steps in turn, each with stages of its own, and their sums are
