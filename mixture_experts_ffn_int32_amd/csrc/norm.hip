@@ -6,9 +6,12 @@
 //   n  = r' rho w, rho   = (mean_H r'^2 + eps)^-1/2     (the next block's pre-norm)
 //
 // and, with t the whole gradient of r' (tr that of its output, dn that of n):
-//   a  = dn w;   t = tr + rho a - r' rho^3 mean(a r');  dr = t
-//   b  = s t g wp;  dy = rho_y b - y rho_y^3 mean(b y)  (dy = b without a post weight)
-//   dw = sum_t dn r' rho;  dwp = sum_t s t g u;  dg = s t wp u, summed over what g is broadcast over
+//   x  = r' rho;   a = dn w;   t = tr + rho (a - x mean(a x));   dr = t
+//   b  = s t g wp;  dy = rho_y (b - u mean(b u))  (dy = b without a post weight)
+//   dw = sum_t dn x;  dwp = sum_t s t g u;  dg = s t wp u, summed over what g is broadcast over
+//
+// The gradients are taken of the normalised rows x and u, at most sqrt(H) in size: rho^3 as a
+// factor of its own leaves float32 for rows of 1e14 and for an eps below 2e-26.
 //
 // n is taken of the stored (rounded) r', so that the backward, which reads the
 // stored r', is the gradient of exactly what the forward computed.
@@ -304,13 +307,14 @@ __global__ void __launch_bounds__(NT == 64 ? 256 : NT) residual_norm_bwd(const N
       w[k].get(wv);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        cw[k][j] = __builtin_fmaf(d[k][j] * rho, r[j], cw[k][j]);
+        const float x = r[j] * rho;
+        cw[k][j] = __builtin_fmaf(d[k][j], x, cw[k][j]);
         d[k][j] *= wv[j];
-        s1[0] = __builtin_fmaf(d[k][j], r[j], s1[0]);
+        s1[0] = __builtin_fmaf(d[k][j], x, s1[0]);
       }
     }
     row_sum<NT>(s1, lds);
-    const float c1 = rho * rho * rho * s1[0] * invH;
+    const float m1 = s1[0] * invH;
 #pragma unroll
     for (int k = 0; k < V; ++k) {
       const int64_t i = (int64_t)(tid + k * NT) * 8;
@@ -319,12 +323,12 @@ __global__ void __launch_bounds__(NT == 64 ? 256 : NT) residual_norm_bwd(const N
       R.tr[k].get(tr[k]);
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        tr[k][j] = __builtin_fmaf(rho, d[k][j], __builtin_fmaf(-c1, r[j], tr[k][j]));
+        tr[k][j] = __builtin_fmaf(rho, __builtin_fmaf(-m1, r[j] * rho, d[k][j]), tr[k][j]);
       if (i < A.H) store8(G.d_residual, RF, t * A.H + i, tr[k], A.stream);
     }
     if (A.y) {  // the same for every thread
       const float rho_y = R.rho_y;
-      float s2[2] = {0.f, 0.f};  // sum b y, sum s t wp u
+      float s2[2] = {0.f, 0.f};  // sum b u, sum s t wp u
 #pragma unroll
       for (int k = 0; k < V; ++k) {
         const int64_t i = (int64_t)(tid + k * NT) * 8;
@@ -345,13 +349,13 @@ __global__ void __launch_bounds__(NT == 64 ? 256 : NT) residual_norm_bwd(const N
           s2[1] += dg[j];
           cp[k][j] = __builtin_fmaf(st * g[j], u, cp[k][j]);
           tr[k][j] = st * g[j] * wpv[j];  // b
-          s2[0] = __builtin_fmaf(tr[k][j], y[j], s2[0]);
+          s2[0] = __builtin_fmaf(tr[k][j], u, s2[0]);
         }
         if (A.gate_kind == NORM_GATE_FULL) store8(G.d_gate, false, t * A.H + i, dg);
       }
       row_sum<NT>(s2, lds);
       if (A.gate_kind == NORM_GATE_TOKEN && tid == 0) static_cast<uint16_t*>(G.d_gate)[t] = f2bf(s2[1]);
-      const float c2 = A.post_weight ? rho_y * rho_y * rho_y * s2[0] * invH : 0.f;
+      const float m2 = A.post_weight ? s2[0] * invH : 0.f;
 #pragma unroll
       for (int k = 0; k < V; ++k) {
         const int64_t i = (int64_t)(tid + k * NT) * 8;
@@ -359,7 +363,7 @@ __global__ void __launch_bounds__(NT == 64 ? 256 : NT) residual_norm_bwd(const N
         float dy[8], y[8];
         R.y[k].get(y);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) dy[j] = __builtin_fmaf(rho_y, tr[k][j], -c2 * y[j]);
+        for (int j = 0; j < 8; ++j) dy[j] = rho_y * __builtin_fmaf(-m2, y[j] * rho_y, tr[k][j]);
         store8(G.d_y, false, t * A.H + i, dy, A.stream);
       }
     }
