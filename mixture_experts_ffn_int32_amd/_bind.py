@@ -8,6 +8,7 @@ the device is switched only if it is another one.
 import contextlib
 
 import torch
+from torch.autograd import forward_ad
 
 _HERE = contextlib.nullcontext()
 
@@ -37,9 +38,12 @@ def ready(t, dtype=None):
 
 
 def check_tensor(name, t, dtypes, dims, device=None):
-    """Type, device, dtype and number of dimensions; ``device``: the one it has to be on."""
+    """Type, device, dtype and number of dimensions; ``device``: the one it has to be on.  A tangent of forward-mode
+    differentiation, which needs no requires_grad and would be lost, is refused."""
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
+    if forward_ad._current_level >= 0 and forward_ad.unpack_dual(t).tangent is not None:
+        raise ValueError("%s has a forward-mode tangent: this operator has no forward-mode derivative" % name)
     if not t.is_cuda:
         raise ValueError("%s must be on a HIP device (got %s)" % (name, t.device))
     if device is not None and t.device != device:

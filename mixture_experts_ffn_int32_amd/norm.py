@@ -130,7 +130,8 @@ def residual_norm(y, residual, norm_weight, *, post_weight=None, gate=None, resi
     residual_out = residual + residual_scale * gate * post_weight * u, rounded to the residual's type;
     normed = residual_out / sqrt(mean(residual_out^2) + eps) * norm_weight, bf16, of the stored residual_out.
     norm_weight and post_weight are [H], both bf16 or both float32; gate is bf16 and multiplies per channel
-    ([H]), per token ([T,1]) or per element ([T,H]).  Sums are float32.  Differentiable in all five tensors.
+    ([H]), per token ([T,1]) or per element ([T,H]).  Sums are float32.  Differentiable in all five tensors,
+    in reverse mode.
     """
     _check_stream("residual", residual)
     T, H = residual.shape
@@ -151,7 +152,7 @@ def residual_norm(y, residual, norm_weight, *, post_weight=None, gate=None, resi
 
 def rms_norm(x, weight, *, eps=1e-6):
     """x / sqrt(mean(x^2) + eps) * weight, bf16: the norm before the first block.  x [T,H] and weight [H], each
-    bf16 or float32; differentiable in both."""
+    bf16 or float32; differentiable in both, in reverse mode."""
     _check_stream("x", x)
     _check_weight("weight", weight, x.shape[1], x.device)
     return _call(None, x, weight, None, None, _lib.HMM_GATE_NONE, 1.0, _check_scalar("eps", eps, True))
