@@ -37,6 +37,12 @@ def ready(t, dtype=None):
     return t.clone() if t.data_ptr() & 15 else t
 
 
+def refuse_gradients(why, *tensors):
+    """ValueError if a gradient of one of the tensors would be asked for (None: no tensor)."""
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
+        raise ValueError(why)
+
+
 def check_tensor(name, t, dtypes, dims, device=None):
     """Type, device, dtype and number of dimensions; ``device``: the one it has to be on.  A tangent of forward-mode
     differentiation, which needs no requires_grad and would be lost, is refused."""

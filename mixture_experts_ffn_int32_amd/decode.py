@@ -9,7 +9,7 @@ import functools
 import torch
 
 from . import _lib
-from ._bind import check_tensor, on_device, ptr, ready, stream_of
+from ._bind import check_tensor, on_device, ptr, ready, refuse_gradients, stream_of
 
 _BF16 = (torch.bfloat16,)
 
@@ -84,9 +84,8 @@ def moe_decode(x, up_proj_weight, down_proj_weight, *, topk_ids=None, topk_weigh
             raise ValueError("topk_ids and topk_weights must both be [T,K] with T = %d (got %s, %s)"
                              % (T, tuple(topk_ids.shape), tuple(topk_weights.shape)))
         K = topk_ids.shape[1]
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (
-            x, up_proj_weight, down_proj_weight, router_weight, topk_weights, up_descale, down_descale)):
-        raise ValueError("moe_decode has no gradient: use hyper_mega_moe, or call it under torch.no_grad()")
+    refuse_gradients("moe_decode has no gradient: use hyper_mega_moe, or call it under torch.no_grad()", x, up_proj_weight,
+                     down_proj_weight, router_weight, topk_weights, up_descale, down_descale)
     prob, nbytes = _problem(T, H, I, E, K, _lib.HMM_FP8_E4M3_BLOCK if fp8 else _lib.HMM_BF16, rdt,
                             _lib.HMM_DECODE_RENORMALIZE if renormalize else 0)
     x = ready(x)

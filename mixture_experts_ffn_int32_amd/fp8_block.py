@@ -12,7 +12,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _lib
-from ._bind import check_tensor, on_device, ptr, ready, stream_of
+from ._bind import check_tensor, on_device, ptr, ready, refuse_gradients, stream_of
 
 GROUP = 128
 _BF16, _U8, _F32 = (torch.bfloat16,), (torch.uint8,), (torch.float32,)
@@ -40,7 +40,7 @@ def quantize_block(w):
     w bf16 [H,N] or [E,H,N], H a multiple of 128 and N of 16 (a last block of columns may be narrower).
     Returns (codes uint8 [(E,) N, H], descale float32 [(E,) ceil(N/128), H/128]): the codes are transposed, so
     that the contraction is contiguous.  Per block, in float32: scale = 448 * (1 / max|block|) (1 for
-    zeros), code = E4M3 of w * scale, descale = 1 / scale."""
+    zeros), code = E4M3 of w * scale, descale = 1 / scale.  Both are detached from w."""
     check_tensor("w", w, _BF16, (2, 3))
     _widths(w.shape[-2], w.shape[-1], 16)
     if w.dim() == 3 and w.shape[0] < 1:
@@ -52,7 +52,7 @@ def quantize_block(w):
 
 def quantize_rows_block(x):
     """The tokens' side: (codes uint8 [T,H], descale float32 [T,H/128]) of x bf16 [T,H], quantize_block's rule per token
-    and group of 128, as linear_fp8_block applies it."""
+    and group of 128, as linear_fp8_block applies it; detached from x."""
     check_tensor("x", x, _BF16, (2,))
     T, H = x.shape
     _widths(GROUP, H, GROUP)
@@ -77,13 +77,14 @@ def _check_codes(codes, descale, H, device):
 
 def matmul_fp8_block(xq, xs, codes, descale):
     """y bf16 [T,N] of tokens (xq uint8 [T,H], xs float32 [T,H/128], as quantize_rows_block gives them) and a weight
-    (codes uint8 [N,H], descale float32 [ceil(N/128),H/128], as quantize_block does)."""
+    (codes uint8 [N,H], descale float32 [ceil(N/128),H/128], as quantize_block does).  It has no gradient."""
     check_tensor("xq", xq, _U8, (2,))
     T, H = xq.shape
     check_tensor("xs", xs, _F32, (2,), xq.device)
     N = _check_codes(codes, descale, H, xq.device)
     if xs.shape != (T, H // GROUP):
         raise ValueError("xs must be [T,H/128] (got %s, T=%d, H=%d)" % (tuple(xs.shape), T, H))
+    refuse_gradients("matmul_fp8_block has no gradient: use linear_fp8_block, or call it under torch.no_grad()", xs, descale)
     dev = xq.device
     with on_device(dev):
         xq, xs, codes, descale = (ready(t) for t in (xq, xs, codes, descale))
@@ -163,7 +164,6 @@ def linear_fp8_block(x, weight):
         raise TypeError("weight must be a bf16 tensor [H,N] or a pair (codes, descale)")
     codes, descale = weight
     N = _check_codes(codes, descale, H, x.device)
-    if torch.is_grad_enabled() and x.requires_grad:
-        raise ValueError("a quantised weight has no gradient: give the bf16 weight, or call under torch.no_grad()")
+    refuse_gradients("a quantised weight has no gradient: give the bf16 weight, or call under torch.no_grad()", x, descale)
     with on_device(x.device):
         return _linear(ready(x), ready(codes), ready(descale), N)
