@@ -398,7 +398,10 @@ hmm_status hmm_quant_cols_group(const void* w, int64_t E, int64_t H, int64_t N, 
  *   normed       bf16 [T,H], may be ``y`` itself
  *   rstd         float32 [2,T] (1/sqrt of the post-norm and of the pre-norm) for the
  *                backward, or NULL
- * T >= 0 rows; H a multiple of 8 in [8, 16384].  All arithmetic is float32.
+ * T >= 0 rows; H a multiple of 8 in [8, 16384].  All arithmetic is float32: a row whose
+ * sum of squares is infinite (an infinite element, or a sum past 3.4e38) has 1 / sqrt = 0,
+ * so that its n (or u) is zero, and NaN where the element is infinite; a NaN makes the
+ * whole row NaN.  Other rows are not touched by it.
  *
  * The backward takes the gradients of the two outputs (either may be NULL: zero) and
  * the stored residual_out, and writes d_y, d_residual (residual_dtype), d_norm_weight
@@ -428,7 +431,7 @@ hmm_status hmm_residual_norm_backward(const hmm_norm_problem* p, const void* d_r
  * SwiGLU, down-projection and weighted sum, reading each chosen expert's weights once.
  * No backward, nothing saved.
  *   l[t,e] = x[t] . router_w[e], in 64 bits; topk_ids[t] = the K largest logits in
- *   descending order (equal logits: the lower expert first; a NaN ranks last);
+ *   descending order (equal logits: the lower expert first; a NaN counts as -infinity);
  *   topk_weights = exp(l - max l) over its sum over the K chosen experts
  *   (HMM_DECODE_RENORMALIZE) or over all E experts;
  *   then hmm_forward's y, with a kept to 16 significant bits and one rounding of y.

@@ -67,7 +67,7 @@ __device__ __forceinline__ void store8(void* p, bool f32, int64_t i, const float
 __device__ __forceinline__ float rsqrt_(float m) {
   const float r = __builtin_amdgcn_rsqf(m);
   const float c = __builtin_fmaf(0.5f * r, __builtin_fmaf(-m * r, r, 1.0f), r);
-  return __builtin_isfinite(c) ? c : r;  // m = 0 (eps = 0) or infinite: the step would make a NaN of it
+  return __builtin_isfinite(c) ? c : r;  // m infinite: 0, of which the step would make a NaN
 }
 
 // sums of N values over the NT threads of a row, in a fixed order, to every thread

@@ -130,8 +130,8 @@ def residual_norm(y, residual, norm_weight, *, post_weight=None, gate=None, resi
     residual_out = residual + residual_scale * gate * post_weight * u, rounded to the residual's type;
     normed = residual_out / sqrt(mean(residual_out^2) + eps) * norm_weight, bf16, of the stored residual_out.
     norm_weight and post_weight are [H], both bf16 or both float32; gate is bf16 and multiplies per channel
-    ([H]), per token ([T,1]) or per element ([T,H]).  Sums are float32.  Differentiable in all five tensors,
-    in reverse mode.
+    ([H]), per token ([T,1]) or per element ([T,H]).  Sums are float32: a row whose sum of squares is
+    infinite has 1 / sqrt = 0.  Differentiable in all five tensors, in reverse mode.
     """
     _check_stream("residual", residual)
     T, H = residual.shape
