@@ -428,8 +428,9 @@ hmm_status hmm_residual_norm_backward(const hmm_norm_problem* p, const void* d_r
                                       void* workspace, size_t workspace_bytes, void* stream);
 
 /* A whole mixture-of-experts layer for a few tokens (serving): router, up-projection,
- * SwiGLU, down-projection and weighted sum, reading each chosen expert's weights once.
- * No backward, nothing saved.
+ * SwiGLU, down-projection and weighted sum.  Each chosen expert's weights are read once
+ * for up to 16 of its rows (tokens), or up to 32 where T > 16 and T K > 8 E, and again for
+ * the next ones.  No backward, nothing saved.
  *   l[t,e] = x[t] . router_w[e], in 64 bits; topk_ids[t] = the K largest logits in
  *   descending order (equal logits: the lower expert first; a NaN counts as -infinity);
  *   topk_weights = exp(l - max l) over its sum over the K chosen experts

@@ -1,10 +1,11 @@
-// A whole mixture-of-experts layer for a few tokens (T <= 64), where every byte
-// of the chosen experts' weights is read once and used for a handful of rows:
+// A whole mixture-of-experts layer for a few tokens (T <= 64), where a chosen
+// expert's weights are streamed for a handful of rows:
 //
 //   l[t,e] = x[t] . Wr[e];  ids[t], w[t] = the K largest logits and their softmax
 //   [g|u]  = x[t] . W1[e];  a = silu(g) u;  y[t] = sum_k w[t,k] a . W2[ids[t,k]]
 //
-// Bound by HBM: an expert's 3 H I weights for 6 H I flop a row.  So nothing of
+// Bound by HBM: an expert's 3 H I weights for 6 H I flop a row, read once for up to 16 or
+// 32 rows (one or two row tiles, launch_experts) and again for the next ones.  So nothing of
 // the large products' tiling is of use here.  A workgroup owns a column tile of
 // one chosen expert; its waves split the contraction, each streaming weights
 // from global memory straight into the matrix instruction's operand registers
@@ -31,7 +32,10 @@
 // (470 MB: 5.3 TB/s), down 47 us (235 MB: 5.0 TB/s); 64 tokens: 6, 5, 334 us (1880 MB: 5.6
 // TB/s), 199 us (940 MB: 4.7 TB/s), sum 6 us.  E = 128, H = 2048, I = 768, 17 tokens: up 89, down
 // 47 us (5.7 and 5.4 TB/s).  E4M3 weights, 8 tokens: up 141 us (5.6 TB/s), down 95 us (4.2
-// TB/s).  Reads alone reach 6.2 TB/s here, a copy 5.2.
+// TB/s).  Reads alone reach 6.2 TB/s here, a copy 5.2.  Experts with more rows than their tiles
+// hold: 64 tokens, 8 experts, K = 4 (24 to 41 rows, 11 passes over 8 experts' weights): up 146 us
+// (655 MB fetched for 470), down 80 (344 for 235); 4 experts, K = 4 (64 rows, every weight twice):
+// 126 and 52 us.
 #include "gemm_common.h"
 #include "kernels.h"
 
