@@ -575,7 +575,12 @@ hipError_t launch_block_gemm(const uint8_t* xq, const float* xs, const uint8_t* 
   // The fewest rounds of the 256 CUs, then the largest tile.  160 tiles of 256 x 256 in one round
   // take 53.9 us against 68.6 of 320 of 256 x 128 in two (5000 x 4096 x 2048); 128 against 256 leave
   // half of the chip idle, 52 to 40 us (4096 x 4096 x 2048).  Below 128 of those, smaller tiles:
-  // 28 against 32.6 us (1536 x 4096 x 2048), at 128 still 35.8 against 34.3 (1024 x 4096 x 4096).
+  // 24.7 against 32.6 us (1536 x 4096 x 2048), at 128 34.5 against 33.2 (1024 x 4096 x 4096).
+  // Between these sizes the product is at 2.5 to 3 times its operations' time.  128 tiles of 256 x 128
+  // take nearly as long as 256 of them (33 and 39 us, 32 steps each): a CU with a tile is at three
+  // quarters of its rate, and half have none.  The small tiles stage four times the bytes a matrix
+  // instruction that 256 x 256 tiles do: 1536 x 4096 x 2048 moves 409 MB into LDS, 16.5 TB/s, matrix
+  // instructions busy a fifth of the time.
   if (tiles(256, 256) > 128) return launch_gemm<BlockTile<256, 256, 4, 2, 2, 1>>(a, stream);
   if (tiles(256, 128) >= 128) return launch_gemm<BlockTile<256, 128, 4, 2, 3, 1>>(a, stream);
   // Small tiles: up to one a CU, two parts of a workgroup share a tile's groups (64 x 7168 x 4096
